@@ -391,6 +391,145 @@ int lcp_deploy_forward(const void* vals, const uint32_t* meta,
                        const int32_t* perm, int B, const void* X, int T,
                        int cout, int cin, void* Xp, void* Y, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Serving operators between the deployed projections of an attention block:
+ * rotary positions, a paged key/value cache (written quantised, read back) and
+ * the attention of one new token over it.
+ *
+ * Head rows. A tensor of T tokens x H heads x D channels is given by its
+ * pointer and the strides (in elements, >= 0) between tokens and between
+ * heads; the D channels of a head are contiguous. Views of a fused projection's
+ * output and head-major layouts are passed as they are. Tensors are read in
+ * 16-byte units where pointer, strides and D allow it, else element by element:
+ * the results are the same.
+ *
+ * Index arrays (positions, slots, page numbers, lengths) are int32 in device
+ * memory; entries outside their range never cause an access outside a buffer:
+ * each entry point says what it does with them.
+ */
+typedef struct lcp_heads {
+  const void* x;           /* input rows                                       */
+  void*       y;           /* output rows, where there are any; may equal x
+                              with equal strides (in place), else must not
+                              overlap it                                       */
+  int         heads;       /* H >= 1                                           */
+  int64_t     x_token, x_head;   /* strides of x, elements                     */
+  int64_t     y_token, y_head;   /* strides of y, elements                     */
+} lcp_heads;
+
+/* Frequencies of the rotary table (lcp_rope_cfg.scaling): pair i of rot_dim / 2
+ * turns by theta_i = base^(-2i / rot_dim) radians a position. */
+#define LCP_ROPE_NONE     0  /* theta_i                                         */
+#define LCP_ROPE_LINEAR   1  /* theta_i / factor                                */
+#define LCP_ROPE_BASE     2  /* base raised to base factor^(r / (r - 2)),
+                                r = rot_dim > 2: the slowest pair turns factor
+                                times slower, the fastest as before            */
+#define LCP_ROPE_BY_PARTS 3  /* n = orig_len theta_i / 2 pi turns in the original
+                                context; g = (n - low_turns) / (high_turns -
+                                low_turns) held to [0, 1];
+                                theta_i (g + (1 - g) / factor)                 */
+typedef struct lcp_rope_cfg {
+  int    rot_dim;                 /* channels rotated, even, 2 .. 1024         */
+  int    scaling;                 /* LCP_ROPE_*                                */
+  double base;                    /* > 1                                       */
+  double factor;                  /* >= 1 (unused by LCP_ROPE_NONE)            */
+  double orig_len;                /* > 0 (LCP_ROPE_BY_PARTS)                   */
+  double low_turns, high_turns;   /* low < high (LCP_ROPE_BY_PARTS)            */
+  double magnitude;               /* > 0: multiplies every cosine and sine     */
+} lcp_rope_cfg;
+
+/* lcp_rope_table - table[p][i] = magnitude (cos(p theta_i), sin(p theta_i)) for
+ * p < max_pos, i < rot_dim / 2, computed in 64 bits and rounded once:
+ * [max_pos][rot_dim / 2][2] fp32, 16-byte aligned. Written once and kept. */
+int lcp_rope_table(const lcp_rope_cfg* rc, int max_pos, float* table, void* stream);
+
+/* lcp_rope - rotary positions of T tokens' queries and (k nullable) keys, in one
+ * launch. Pair i < rot_dim / 2 of a head is channels (i, i + rot_dim / 2), or
+ * (2i, 2i + 1) when interleaved; with (c, s) = table[pos[t]][i]
+ *   a' = a c - b s,  b' = b c + a s;     inverse != 0: s taken as -s.
+ * inverse = 1 is the transpose, so it turns dL/dy into dL/dx (the gradient, and
+ * the inverse rotation for magnitude 1). Channels from rot_dim on are copied.
+ * fp32 arithmetic, one rounding to dt.
+ *   dt F32 or BF16; D in 2 .. 1024, rot_dim even, 2 .. D; pos[t] is held to
+ *   [0, max_pos - 1]; strides of y must keep its rows apart. */
+int lcp_rope(const lcp_heads* q, const lcp_heads* k, lcp_dtype dt, int T, int D,
+             const float* table, int max_pos, const int32_t* pos, int rot_dim,
+             int interleaved, int inverse, void* stream);
+
+/* Cache formats: what one stored element is. The 8-bit formats hold one fp32
+ * scale for each (slot, head) of K and of V; the value is code * scale. For a
+ * row x of D fp32 numbers with a = max |x_d|:
+ *   E4M3: scale = the least power of two with a / scale <= 448, not under
+ *         2^-126; code = x / scale rounded to e4m3 (nearest even).
+ *   INT8: scale = max(a / 127, 2^-126); code = x / scale rounded to nearest
+ *         even, held to [-127, 127].
+ * A row with an infinity or a NaN is stored with a NaN scale, so that it reads
+ * back as NaN and never as numbers that look right. */
+#define LCP_KV_BF16 0
+#define LCP_KV_E4M3 1
+#define LCP_KV_INT8 2
+
+/* A paged cache (host struct of device pointers, all owned by the caller). */
+typedef struct lcp_kv_cache {
+  void*  k;         /* [pages][heads][page_size][D] in the format             */
+  void*  v;         /* the same                                               */
+  float* k_scale;   /* [pages][heads][page_size], 8-bit formats, else NULL    */
+  float* v_scale;   /* the same                                               */
+  int    format;    /* LCP_KV_*                                               */
+  int    pages;     /* pages * page_size < 2^31                               */
+  int    page_size; /* a multiple of 16, up to 4096                           */
+  int    heads;     /* key/value heads                                        */
+  int    D;         /* 64, 128 or 256                                         */
+} lcp_kv_cache;     /* pointers 16-byte aligned                               */
+
+/* lcp_kv_append - write T tokens' keys and values into the cache, quantised to
+ * its format, and rotate their queries, in one launch. With a table, K is
+ * rotated first (lcp_rope's rotation, in fp32, not rounded before it is
+ * quantised) and q (nullable) is rotated into q->y; without a table (NULL) K is
+ * stored as it is and q must be NULL.
+ *   q, k, v: bf16 head rows; k->heads = v->heads = the cache's; k->y and v->y
+ *   are not used. slots[t] = page * page_size + offset of token t; a slot
+ *   outside the cache writes nothing (its query is still rotated); two tokens
+ *   of one call must not share a slot. pos as for lcp_rope. rot_dim a multiple
+ *   of 16, up to D. */
+int lcp_kv_append(const lcp_kv_cache* c, const lcp_heads* q, const lcp_heads* k,
+                  const lcp_heads* v, int T, const int32_t* slots,
+                  const float* table, int max_pos, const int32_t* pos,
+                  int rot_dim, int interleaved, void* stream);
+
+/* lcp_kv_read - read T slots back: k_out and v_out [T][heads][D] in odt (F32 or BF16;
+ * code * scale in fp32, then rounded to odt), 16-byte aligned. A slot outside the cache
+ * reads as zeros. */
+int lcp_kv_read(const lcp_kv_cache* c, const int32_t* slots, int T, void* k_out,
+                void* v_out, lcp_dtype odt, void* stream);
+
+/* lcp_attn_decode - attention of one new token of each of B sequences over the
+ * cache. Query head h reads key/value head h / (hq / heads). With n = lens[b]
+ * and t from max(0, n - window) (window 0: from 0) to n - 1,
+ *   z_t = scale q.k_t,  m = max z,  l = sum exp(z_t - m),
+ *   out = sum exp(z_t - m) v_t / l,  lse = m + ln l.
+ * A sequence without tokens gives out 0 and lse -inf. What the cache holds in
+ * other slots (the rest of a last page, freed pages) has no effect, whatever
+ * its bits. The sums are fp32; the work is split over the tokens and joined in
+ * a fixed order, so equal inputs give equal bits.
+ *   q: bf16 [B][hq][D] with q_row elements between sequences (>= hq D), heads
+ *   adjacent, 16-byte aligned rows; hq a multiple of heads.
+ *   pages: [B][max_pages], the page number of tokens page_size i ..; entries
+ *   that no counted token needs are not read; tokens of a page number outside
+ *   the cache are left out. lens[b] is held to [0, max_len]; max_len <= max_pages
+ *   page_size is the caller's bound, from which the split is chosen.
+ *   out: [B][hq][D] in odt (F32 or BF16), 16-byte aligned; lse (nullable):
+ *   [B][hq] fp32. scale finite. window >= 0.
+ *   ws: lcp_attn_decode_workspace_bytes bytes, 256-byte aligned; one workspace
+ *   serves one call in flight. */
+int lcp_attn_decode_workspace_bytes(const lcp_kv_cache* c, int B, int hq,
+                                    int max_len, int window, size_t* bytes);
+int lcp_attn_decode(const lcp_kv_cache* c, const void* q, int64_t q_row, int B,
+                    int hq, const int32_t* pages, int max_pages,
+                    const int32_t* lens, int max_len, float scale, int window,
+                    void* out, lcp_dtype odt, float* lse, void* ws,
+                    size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -14,9 +14,11 @@ from ._lib import (LCP_BF16, LCP_F32, LcpError, lcp_colnorm, lcp_error,  # noqa:
                    lcp_error_workspace_bytes, lcp_harden, lcp_layer_init, lcp_nm_mask, lcp_permute,
                    lcp_sinkhorn, lcp_sinkhorn_bwd, lcp_step_bwd, lcp_step_fwd,
                    lcp_step_workspace_bytes, lcp_xt_pitch, make_cfg, make_layer, make_timing,
-                   lcp_adamw, lcp_step_bwd_adamw, lcp_train, make_adamw_cfg, lcp_layer_outputs)
+                   lcp_adamw, lcp_step_bwd_adamw, lcp_train, make_adamw_cfg, lcp_layer_outputs,
+                   lcp_attn_decode, lcp_attn_decode_workspace_bytes, lcp_kv_append, lcp_kv_read, lcp_rope,
+                   lcp_rope_table, make_kv_cache, make_rope_cfg)
 
-__all__ = ["LayerSession", "LcpError"] + [n for n in _lib.EXPORTS if n.startswith("lcp_")]
+__all__ = ["LayerSession", "LcpError", "PagedKVCache"] + [n for n in _lib.EXPORTS if n.startswith("lcp_")]
 
 
 class LayerSession:
@@ -111,3 +113,67 @@ class LayerSession:
         lcp_train(self.layer, logits, self.cfg, self.ws, m, v, steps, tau0, tau1, acfg, errs, stream)
         return errs
 
+
+
+def _used_on(stream, t):
+    """A new tensor that a call on `stream` (None: the current one, which torch
+    orders by itself) uses: its memory is not given away before that stream is done with it."""
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+class PagedKVCache:
+    """A paged key/value cache on one GPU and the attention that reads it.
+
+    k, v: pages [pages, heads, page_size, D] in bfloat16, float8_e4m3fn or
+    int8 (the 8-bit formats with fp32 scales [pages, heads, page_size]); D 64,
+    128 or 256, page_size a multiple of 16. Which pages belong to which
+    sequence is the caller's: slots (page * page_size + offset) say where new
+    tokens go, a page table [B, max_pages] and the lengths what a step reads.
+    """
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.c = make_kv_cache(k, v, k_scale, v_scale)
+
+    @classmethod
+    def empty(cls, pages, page_size, heads, D, dtype=torch.float8_e4m3fn, device="cuda"):
+        """A cache with room for pages * page_size tokens (its contents are undefined until written)."""
+        k, v = (torch.empty((pages, heads, page_size, D), dtype=dtype, device=device) for _ in range(2))
+        ks = vs = None
+        if dtype != torch.bfloat16:
+            ks, vs = (torch.empty((pages, heads, page_size), dtype=torch.float32, device=device) for _ in range(2))
+        return cls(k, v, ks, vs)
+
+    def append(self, k, v, slots, q=None, q_out=None, table=None, pos=None, interleaved=False, stream=None):
+        """Write new tokens' k and v [T, heads, D] (k rotated by the table at pos first) and rotate q [T, hq, D]
+        into q_out (lcp_kv_append)."""
+        lcp_kv_append(self.c, k, v, slots, q, q_out, table, pos, interleaved, stream)
+        return q_out
+
+    def read(self, slots, k_out=None, v_out=None, stream=None):
+        """The stored k and v of slots, [T, heads, D] bfloat16 unless outputs are given (lcp_kv_read)."""
+        shape = (slots.shape[0], self.c.heads, self.c.D)
+        if k_out is None:
+            k_out = _used_on(stream, torch.empty(shape, dtype=torch.bfloat16, device=slots.device))
+        if v_out is None:
+            v_out = _used_on(stream, torch.empty(shape, dtype=k_out.dtype, device=slots.device))
+        lcp_kv_read(self.c, slots, k_out, v_out, stream)
+        return k_out, v_out
+
+    def attend(self, q, pages, lens, max_len=None, scale=None, window=0, out=None, lse=None, ws=None, stream=None):
+        """Attention of one new token of each sequence, q [B, hq, D] bfloat16 (lcp_attn_decode): (out, lse). max_len,
+        the host's bound on lens, defaults to what the page table can hold; scale to D^-1/2."""
+        B, hq, _ = q.shape
+        if max_len is None:
+            max_len = pages.shape[1] * self.c.page_size
+        if out is None:
+            out = _used_on(stream, torch.empty(q.shape, dtype=torch.bfloat16, device=q.device))
+        if lse is None:
+            lse = _used_on(stream, torch.empty((B, hq), dtype=torch.float32, device=q.device))
+        if ws is None:
+            n = lcp_attn_decode_workspace_bytes(self.c, B, hq, max_len, window)
+            ws = _used_on(stream, torch.empty(n, dtype=torch.uint8, device=q.device))
+        lcp_attn_decode(self.c, q, pages, lens, max_len, out, ws, lse, scale, window, stream)
+        return out, lse

@@ -29,6 +29,15 @@ LCP_NOALLOC_MAX_PARTS = 16384   # partial sums held by lcp_layer_outputs_noalloc
 LCP_F32 = 0
 LCP_BF16 = 1
 
+LCP_ROPE_NONE = 0
+LCP_ROPE_LINEAR = 1
+LCP_ROPE_BASE = 2
+LCP_ROPE_BY_PARTS = 3
+
+LCP_KV_BF16 = 0
+LCP_KV_E4M3 = 1
+LCP_KV_INT8 = 2
+
 LCP_LOSS_FROBENIUS = 0
 LCP_LOSS_COSINE = 1
 
@@ -38,7 +47,8 @@ EXPORTS = [
     "lcp_error_workspace_bytes", "lcp_error", "lcp_step_workspace_bytes", "lcp_step_fwd",
     "lcp_step_bwd", "lcp_harden", "lcp_adamw", "lcp_step_bwd_adamw", "lcp_train",
     "lcp_layer_outputs", "lcp_layer_outputs_noalloc", "lcp_sparse_pack_bytes", "lcp_sparse_pack", "lcp_gather_channels",
-    "lcp_sparse_gemm", "lcp_deploy_forward",
+    "lcp_sparse_gemm", "lcp_deploy_forward", "lcp_rope_table", "lcp_rope", "lcp_kv_append", "lcp_kv_read",
+    "lcp_attn_decode_workspace_bytes", "lcp_attn_decode",
 ]
 
 
@@ -62,6 +72,24 @@ class lcp_adamw_cfg(ctypes.Structure):
 
 class lcp_timing(ctypes.Structure):
     _fields_ = [("start", ctypes.c_void_p * 8), ("stop", ctypes.c_void_p * 8)]
+
+
+class lcp_heads(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("heads", ctypes.c_int),
+                ("x_token", ctypes.c_int64), ("x_head", ctypes.c_int64),
+                ("y_token", ctypes.c_int64), ("y_head", ctypes.c_int64)]
+
+
+class lcp_rope_cfg(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int), ("scaling", ctypes.c_int), ("base", ctypes.c_double),
+                ("factor", ctypes.c_double), ("orig_len", ctypes.c_double), ("low_turns", ctypes.c_double),
+                ("high_turns", ctypes.c_double), ("magnitude", ctypes.c_double)]
+
+
+class lcp_kv_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("format", ctypes.c_int), ("pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("heads", ctypes.c_int), ("D", ctypes.c_int)]
 
 
 class LcpError(RuntimeError):
@@ -102,6 +130,14 @@ def _load():
         "lcp_gather_channels": (i, [vp, i, i, i, vp, vp, vp]),
         "lcp_sparse_gemm": (i, [vp, vp, vp, i, i, i, vp, vp]),
         "lcp_deploy_forward": (i, [vp, vp, vp, i, vp, i, i, i, vp, vp, vp]),
+        "lcp_rope_table": (i, [ctypes.POINTER(lcp_rope_cfg), i, vp, vp]),
+        "lcp_rope": (i, [ctypes.POINTER(lcp_heads), ctypes.POINTER(lcp_heads), i, i, i, vp, i, vp, i, i, i, vp]),
+        "lcp_kv_append": (i, [ctypes.POINTER(lcp_kv_cache), ctypes.POINTER(lcp_heads), ctypes.POINTER(lcp_heads),
+                              ctypes.POINTER(lcp_heads), i, vp, vp, i, vp, i, i, vp]),
+        "lcp_kv_read": (i, [ctypes.POINTER(lcp_kv_cache), vp, i, vp, vp, i, vp]),
+        "lcp_attn_decode_workspace_bytes": (i, [ctypes.POINTER(lcp_kv_cache), i, i, i, i, psz]),
+        "lcp_attn_decode": (i, [ctypes.POINTER(lcp_kv_cache), vp, ctypes.c_int64, i, i, vp, i, vp, i, f, i, vp, i, vp,
+                                vp, sz, vp]),
         "lcp_step_workspace_bytes": (i, [i, i, i, i, i, i, psz]),
         "lcp_step_fwd": (i, [ctypes.POINTER(lcp_layer), vp, ctypes.POINTER(lcp_cfg), vp, sz, vp, vp, vp,
                              ctypes.POINTER(lcp_timing), vp]),
@@ -318,3 +354,130 @@ def lcp_deploy_forward(vals, meta, perm, B, X, cout, Xp, Y, stream=None):
     T, cin = X.shape
     return _check("lcp_deploy_forward", LIB.lcp_deploy_forward(_p(vals), _p(meta), _p(perm), int(B), _p(X), T,
                                                                int(cout), cin, _p(Xp), _p(Y), _stream(stream)))
+
+
+# ---- serving operators --------------------------------------------------------
+_KV_FORMATS = {torch.bfloat16: LCP_KV_BF16, torch.float8_e4m3fn: LCP_KV_E4M3, torch.int8: LCP_KV_INT8}
+
+
+def _index(t, shape, name):
+    """A device int32 index array of the given shape."""
+    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError("%s must be contiguous int32 of shape %s" % (name, shape))
+    return t.data_ptr()
+
+
+def _heads(x, y, D, dtype, name):
+    """Head rows [T, heads, D] (any strides, channels contiguous)."""
+    if x.dim() != 3 or x.shape[2] != D or x.stride(2) != 1 or x.dtype != dtype:
+        raise ValueError("%s must be [T, heads, %d] %s with contiguous channels" % (name, D, dtype))
+    st, sh, _ = x.stride()
+    if y is None:
+        return lcp_heads(x.data_ptr(), None, x.shape[1], st, sh, 0, 0)
+    if y.shape != x.shape or y.stride(2) != 1 or y.dtype != dtype:
+        raise ValueError("the output of %s must have its shape and dtype and contiguous channels" % name)
+    yt, yh, _ = y.stride()
+    return lcp_heads(x.data_ptr(), y.data_ptr(), x.shape[1], st, sh, yt, yh)
+
+
+def _table(table):
+    """A rotary table [max_pos, rot_dim / 2, 2] -> (pointer, max_pos, rot_dim)."""
+    if table.dim() != 3 or table.shape[2] != 2 or table.dtype != torch.float32 or not table.is_contiguous():
+        raise ValueError("table must be contiguous float32 [max_pos, rot_dim / 2, 2]")
+    return table.data_ptr(), table.shape[0], 2 * table.shape[1]
+
+
+def make_rope_cfg(rot_dim, base=10000.0, scaling="none", factor=1.0, orig_len=0.0, low_turns=1.0, high_turns=32.0,
+                  magnitude=1.0):
+    codes = {"none": LCP_ROPE_NONE, "linear": LCP_ROPE_LINEAR, "base": LCP_ROPE_BASE, "by_parts": LCP_ROPE_BY_PARTS}
+    return lcp_rope_cfg(int(rot_dim), codes[scaling], float(base), float(factor), float(orig_len), float(low_turns),
+                        float(high_turns), float(magnitude))
+
+
+def lcp_rope_table(cfg, table, stream=None):
+    p, max_pos, rot = _table(table)
+    if rot != cfg.rot_dim:
+        raise ValueError("table holds %d rotated channels, the configuration %d" % (rot, cfg.rot_dim))
+    return _check("lcp_rope_table", LIB.lcp_rope_table(ctypes.byref(cfg), max_pos, p, _stream(stream)))
+
+
+def lcp_rope(q, q_out, table, pos, k=None, k_out=None, interleaved=False, inverse=False, stream=None):
+    T, _, D = q.shape
+    hq = _heads(q, q_out, D, q.dtype, "q")
+    hk = None
+    if k is not None:
+        if k.shape[0] != T or k_out is None:
+            raise ValueError("k needs q's number of tokens and an output")
+        hk = ctypes.byref(_heads(k, k_out, D, q.dtype, "k"))
+    p, max_pos, rot = _table(table)
+    return _check("lcp_rope", LIB.lcp_rope(ctypes.byref(hq), hk, dtype_code(q), T, D, p, max_pos,
+                                           _index(pos, (T,), "pos"), rot, 1 if interleaved else 0, 1 if inverse else 0,
+                                           _stream(stream)))
+
+
+def make_kv_cache(k, v, k_scale=None, v_scale=None):
+    """lcp_kv_cache over pages [pages, heads, page_size, D] (bfloat16, float8_e4m3fn or int8) and, for the 8-bit
+    formats, scales [pages, heads, page_size]."""
+    if k.dtype not in _KV_FORMATS:
+        raise TypeError("unsupported cache dtype %s" % k.dtype)
+    if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or not (k.is_contiguous() and v.is_contiguous()):
+        raise ValueError("k and v must be contiguous [pages, heads, page_size, D] of one dtype")
+    pages, heads, ps, D = k.shape
+    sk = sv = None
+    if k.dtype != torch.bfloat16:
+        if k_scale is None or v_scale is None:
+            raise ValueError("8-bit caches need k_scale and v_scale")
+        for s in (k_scale, v_scale):
+            if s.dtype != torch.float32 or tuple(s.shape) != (pages, heads, ps) or not s.is_contiguous():
+                raise ValueError("scales must be contiguous float32 [pages, heads, page_size]")
+        sk, sv = k_scale.data_ptr(), v_scale.data_ptr()
+    return lcp_kv_cache(k.data_ptr(), v.data_ptr(), sk, sv, _KV_FORMATS[k.dtype], pages, ps, heads, D)
+
+
+def lcp_kv_append(cache, k, v, slots, q=None, q_out=None, table=None, pos=None, interleaved=False, stream=None):
+    T = k.shape[0]
+    hk, hv = _heads(k, None, cache.D, torch.bfloat16, "k"), _heads(v, None, cache.D, torch.bfloat16, "v")
+    if v.shape[0] != T or (q is not None and (q.shape[0] != T or q_out is None or table is None)):
+        raise ValueError("q, k and v need one number of tokens, and q an output and a table")
+    hq = None if q is None else ctypes.byref(_heads(q, q_out, cache.D, torch.bfloat16, "q"))
+    p, max_pos, rot = (None, 0, 0) if table is None else _table(table)
+    pp = None if table is None else _index(pos, (T,), "pos")
+    return _check("lcp_kv_append", LIB.lcp_kv_append(ctypes.byref(cache), hq, ctypes.byref(hk), ctypes.byref(hv), T,
+                                                     _index(slots, (T,), "slots"), p, max_pos, pp, rot,
+                                                     1 if interleaved else 0, _stream(stream)))
+
+
+def lcp_kv_read(cache, slots, k_out, v_out, stream=None):
+    T = slots.shape[0]
+    for x in (k_out, v_out):
+        if tuple(x.shape) != (T, cache.heads, cache.D) or x.dtype != k_out.dtype or not x.is_contiguous():
+            raise ValueError("k_out and v_out must be contiguous [T, heads, D] of one dtype")
+    return _check("lcp_kv_read", LIB.lcp_kv_read(ctypes.byref(cache), _index(slots, (T,), "slots"), T,
+                                                 k_out.data_ptr(), v_out.data_ptr(), dtype_code(k_out),
+                                                 _stream(stream)))
+
+
+def lcp_attn_decode_workspace_bytes(cache, B, hq, max_len, window=0):
+    out = ctypes.c_size_t(0)
+    _check("lcp_attn_decode_workspace_bytes",
+           LIB.lcp_attn_decode_workspace_bytes(ctypes.byref(cache), int(B), int(hq), int(max_len), int(window),
+                                               ctypes.byref(out)))
+    return out.value
+
+
+def lcp_attn_decode(cache, q, pages, lens, max_len, out, ws, lse=None, scale=None, window=0, stream=None):
+    B, hq, D = q.shape
+    if q.dtype != torch.bfloat16 or D != cache.D or q.stride(2) != 1 or (hq > 1 and q.stride(1) != D):
+        raise ValueError("q must be [B, heads, %d] bfloat16 with adjacent heads" % cache.D)
+    if out.shape != q.shape or not out.is_contiguous():
+        raise ValueError("out must be contiguous and have q's shape")
+    if lse is not None and (tuple(lse.shape) != (B, hq) or lse.dtype != torch.float32 or not lse.is_contiguous()):
+        raise ValueError("lse must be contiguous float32 [B, heads]")
+    row = q.stride(0) if B > 1 else hq * D
+    P = pages.shape[1]
+    return _check("lcp_attn_decode",
+                  LIB.lcp_attn_decode(ctypes.byref(cache), q.data_ptr(), row, B, hq, _index(pages, (B, P), "pages"), P,
+                                      _index(lens, (B,), "lens"), int(max_len), D ** -0.5 if scale is None else scale,
+                                      int(window), out.data_ptr(), dtype_code(out),
+                                      None if lse is None else lse.data_ptr(), ws.data_ptr(),
+                                      ws.numel() * ws.element_size(), _stream(stream)))

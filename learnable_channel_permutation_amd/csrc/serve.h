@@ -1,0 +1,72 @@
+// Serving operators of an attention block (rotary positions, paged key/value
+// cache, one-token attention): arguments of their launchers. Validation is done
+// by serve.hip before any launcher runs; every launcher enqueues on `s` and
+// returns hipGetLastError().
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "common.h"
+
+namespace lcp {
+
+// Head rows [T][heads][D] with strides in elements, input and output.
+struct Rows {
+  const void* x;
+  void* y;
+  int heads;
+  int64_t xt, xh, yt, yh;
+};
+
+struct RopeArgs {
+  Rows q, k;             // k.heads == 0: queries only
+  int T, D, rot, max_pos;
+  int interleaved, inverse;
+  const float2* table;   // [max_pos][rot / 2] (cos, sin)
+  const int* pos;
+};
+hipError_t launch_rope(const RopeArgs& a, int bf16, hipStream_t s);
+
+struct RopeFreq {        // theta_i of the table, see lcp_rope_cfg
+  int rot, scaling;
+  double base, factor, orig_len, low, high, mag;
+};
+hipError_t launch_rope_table(const RopeFreq& f, int max_pos, float2* table, hipStream_t s);
+
+enum KvFormat { KV_BF16 = 0, KV_E4M3 = 1, KV_INT8 = 2 };
+struct KvCache {
+  void *k, *v;           // [pages][heads][page_size][D]
+  float *ks, *vs;        // [pages][heads][page_size]
+  int format, pages, ps, heads, D;
+};
+
+struct KvAppendArgs {
+  KvCache c;
+  Rows q, k, v;          // bf16; q.heads == 0: no queries
+  int T, rot, max_pos, interleaved;   // rot == 0: K stored as it is
+  const int* slots;
+  const float2* table;
+  const int* pos;
+};
+hipError_t launch_kv_append(const KvAppendArgs& a, hipStream_t s);
+hipError_t launch_kv_read(const KvCache& c, const int* slots, int T, void* k, void* v, int bf16, hipStream_t s);
+
+struct AttnArgs {
+  KvCache c;
+  const uint16_t* q;     // [B][hq][D], qrow elements between sequences
+  int64_t qrow;
+  int B, hq, max_pages, max_len, window;
+  const int* pages;
+  const int* lens;
+  float scale2;          // softmax scale x log2 e
+  void* out;             // [B][hq][D]
+  int out_bf16;
+  float* lse;            // nullable
+  float* ws;
+};
+size_t attn_workspace_bytes(const KvCache& c, int B, int hq, int max_len, int window);
+hipError_t launch_attn_decode(const AttnArgs& a, hipStream_t s);
+
+}  // namespace lcp

@@ -1,0 +1,171 @@
+"""Refusals of the serving entry points (no GPU: every call is rejected before
+any HIP call) and the argument checks of their Python forms."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+P = 0x100000
+
+
+def _lib():
+    from learnable_channel_permutation_amd import _lib as L
+    return L
+
+
+def _rows(L, heads=4, x=P, y=2 * P, xt=512, xh=128, yt=512, yh=128):
+    return L.lcp_heads(x, y, heads, xt, xh, yt, yh)
+
+
+def test_rope_table_refusals():
+    L = _lib()
+
+    def call(n=10, table=P, **kw):
+        return L.LIB.lcp_rope_table(ctypes.byref(L.make_rope_cfg(**{"rot_dim": 64, **kw})), n, table, None)
+
+    for bad in (dict(rot_dim=0), dict(rot_dim=7), dict(base=1.0), dict(base=math.nan), dict(magnitude=0.0),
+                dict(magnitude=math.inf), dict(n=0), dict(table=None), dict(table=P + 4), dict(n=1 << 27),
+                dict(scaling="linear", factor=0.5), dict(scaling="linear", factor=math.inf),
+                dict(scaling="base", factor=2.0, rot_dim=2), dict(scaling="by_parts", factor=2.0),
+                dict(scaling="by_parts", factor=2.0, orig_len=10.0, low_turns=4.0, high_turns=4.0)):
+        assert call(**bad) == L.LCP_E_INVAL, bad
+    assert call(rot_dim=1026) == L.LCP_E_UNSUPPORTED
+    c = L.make_rope_cfg(64)
+    c.scaling = 9
+    assert L.LIB.lcp_rope_table(ctypes.byref(c), 10, P, None) == L.LCP_E_UNSUPPORTED
+    assert L.LIB.lcp_rope_table(None, 10, P, None) == L.LCP_E_INVAL
+
+
+def test_rope_refusals():
+    L = _lib()
+
+    def call(q=None, k=None, dt=L.LCP_BF16, T=5, D=128, table=P, n=10, pos=P, rot=128, inter=0, inv=0):
+        q = _rows(L) if q is None else q
+        return L.LIB.lcp_rope(ctypes.byref(q), None if k is None else ctypes.byref(k), dt, T, D, table, n, pos, rot,
+                              inter, inv, None)
+
+    for bad in (dict(T=0), dict(T=-1), dict(table=None), dict(table=P + 8), dict(pos=None), dict(n=0), dict(rot=0),
+                dict(rot=63), dict(rot=130), dict(D=1, rot=1), dict(inter=2), dict(inv=-1),
+                dict(q=_rows(L, heads=0)), dict(q=_rows(L, x=0)), dict(q=_rows(L, y=0)), dict(q=_rows(L, x=P + 1)),
+                dict(q=_rows(L, xt=-512)), dict(q=_rows(L, yt=500)), dict(q=_rows(L, yh=127)), dict(q=_rows(L, yt=0)),
+                dict(q=_rows(L, x=P, y=P, xt=1024)), dict(k=_rows(L, x=0)), dict(k=_rows(L, yt=100)),
+                dict(dt=L.LCP_F32, q=_rows(L, x=P + 2)), dict(q=_rows(L, xt=1 << 50))):
+        assert call(**bad) == L.LCP_E_INVAL, bad
+    assert call(dt=7) == L.LCP_E_UNSUPPORTED
+    assert call(D=1026, rot=64, q=_rows(L, yt=1 << 20, yh=1 << 11)) == L.LCP_E_UNSUPPORTED
+    assert L.LIB.lcp_rope(None, None, L.LCP_BF16, 1, 64, P, 1, P, 64, 0, 0, None) == L.LCP_E_INVAL
+
+
+def _cache(L, **kw):
+    f = dict(k=P, v=2 * P, k_scale=3 * P, v_scale=4 * P, format=L.LCP_KV_E4M3, pages=10, page_size=16, heads=4, D=128)
+    f.update(kw)
+    return L.lcp_kv_cache(*[f[n] for n, _ in L.lcp_kv_cache._fields_])
+
+
+BAD_CACHE = [(dict(k=None), -1), (dict(v=None), -1), (dict(v=P), -1), (dict(k=P + 8), -1), (dict(k_scale=None), -1),
+             (dict(v_scale=P + 4), -1), (dict(pages=0), -1), (dict(heads=0), -1), (dict(D=-64), -1),
+             (dict(page_size=0), -1), (dict(pages=1 << 27), -1), (dict(format=3), -2), (dict(format=-1), -2),
+             (dict(D=96), -2), (dict(page_size=24), -2), (dict(page_size=8192), -2)]
+
+
+@pytest.mark.parametrize("bad,code", BAD_CACHE)
+def test_cache_refusals(bad, code):
+    L = _lib()
+    c = ctypes.byref(_cache(L, **bad))
+    r = _rows(L)
+    assert L.LIB.lcp_kv_append(c, None, ctypes.byref(r), ctypes.byref(r), 3, P, None, 0, None, 0, 0, None) == code
+    assert L.LIB.lcp_kv_read(c, P, 3, P, 2 * P, L.LCP_BF16, None) == code
+    n = ctypes.c_size_t(0)
+    assert L.LIB.lcp_attn_decode_workspace_bytes(c, 1, 4, 100, 0, ctypes.byref(n)) == code
+    assert L.LIB.lcp_attn_decode(c, P, 512, 1, 4, P, 10, P, 100, 0.1, 0, P, L.LCP_BF16, None, P, 1 << 30, None) == code
+
+
+def test_append_and_read_refusals():
+    L = _lib()
+
+    def app(q=None, k="d", v="d", T=3, slots=P, table=P, n=10, pos=P, rot=128, inter=0, c=None):
+        k, v = (_rows(L) if x == "d" else x for x in (k, v))
+        r = lambda x: None if x is None else ctypes.byref(x)       # noqa: E731
+        return L.LIB.lcp_kv_append(r(c or _cache(L)), r(q), r(k), r(v), T, slots, table, n, pos, rot, inter, None)
+
+    for bad in (dict(k=None), dict(v=None), dict(T=0), dict(slots=None), dict(k=_rows(L, heads=3)),
+                dict(v=_rows(L, heads=5)), dict(k=_rows(L, x=P + 1)), dict(v=_rows(L, x=0)), dict(pos=None), dict(n=0),
+                dict(rot=0), dict(rot=144), dict(inter=3), dict(table=P + 4), dict(q=_rows(L, y=0)),
+                dict(q=_rows(L), table=None), dict(q=_rows(L, yt=100))):
+        assert app(**bad) == L.LCP_E_INVAL, bad
+    assert app(rot=24) == L.LCP_E_UNSUPPORTED
+    c = ctypes.byref(_cache(L))
+    rd = L.LIB.lcp_kv_read
+    assert rd(c, None, 3, P, 2 * P, 1, None) == L.LCP_E_INVAL
+    assert rd(c, P, 0, P, 2 * P, 1, None) == L.LCP_E_INVAL
+    assert rd(c, P, 3, None, 2 * P, 1, None) == L.LCP_E_INVAL
+    assert rd(c, P, 3, P, P, 1, None) == L.LCP_E_INVAL
+    assert rd(c, P, 3, P + 8, 2 * P, 1, None) == L.LCP_E_INVAL
+    assert rd(c, P, 3, P, 2 * P, 5, None) == L.LCP_E_UNSUPPORTED
+
+
+def test_attend_refusals():
+    L = _lib()
+
+    def call(q=P, row=512, B=2, hq=4, pages=P, mp=10, lens=P, ml=100, scale=0.1, window=0, out=P, odt=1, lse=None,
+             ws=P, n=1 << 30):
+        return L.LIB.lcp_attn_decode(ctypes.byref(_cache(L)), q, row, B, hq, pages, mp, lens, ml, scale, window, out,
+                                     odt, lse, ws, n, None)
+
+    for bad in (dict(q=None), dict(q=P + 8), dict(row=504), dict(row=516), dict(B=0), dict(hq=0), dict(hq=6),
+                dict(pages=None), dict(mp=0), dict(lens=None), dict(ml=-1), dict(ml=161), dict(scale=math.nan),
+                dict(scale=math.inf), dict(window=-1), dict(out=None), dict(out=P + 4), dict(lse=P + 2), dict(ws=None),
+                dict(B=1 << 23)):
+        assert call(**bad) == L.LCP_E_INVAL, bad
+    assert call(odt=4) == L.LCP_E_UNSUPPORTED
+    assert call(ws=P + 128) == L.LCP_E_WORKSPACE
+    assert call(n=0) == L.LCP_E_WORKSPACE
+    c = _cache(L)
+    need = L.lcp_attn_decode_workspace_bytes(c, 2, 4, 160)
+    assert need > 0 and call(ml=160, n=need - 1) == L.LCP_E_WORKSPACE
+    with pytest.raises(L.LcpError) as e:
+        L.lcp_attn_decode_workspace_bytes(c, 0, 4, 160)
+    assert e.value.code == L.LCP_E_INVAL
+    assert L.LIB.lcp_attn_decode_workspace_bytes(ctypes.byref(c), 2, 4, 160, 0, None) == L.LCP_E_INVAL
+
+
+def test_python_forms_check_shapes_and_types():
+    """Wrong dtypes, shapes and layouts are errors in Python, not reads of something else."""
+    import learnable_channel_permutation_amd as lcp
+    bf = torch.bfloat16
+    x, t = torch.zeros(3, 2, 64, dtype=bf), torch.zeros(9, 32, 2)
+    pos = torch.zeros(3, dtype=torch.int32)
+    for kw in (dict(pos=pos.long()), dict(pos=pos[:2]), dict(table=t.double()), dict(table=t[:, ::2]),
+               dict(q=x.transpose(1, 2)), dict(q_out=x[:2]), dict(q_out=x.float()), dict(k=x),
+               dict(k=x[:2], k_out=x[:2]), dict(k=x.float(), k_out=x.float())):
+        a = {**dict(q=x, q_out=torch.empty_like(x), table=t, pos=pos), **kw}
+        with pytest.raises(ValueError):
+            lcp.lcp_rope(**a)
+    with pytest.raises(TypeError):
+        h = x.half()
+        lcp.lcp_rope(h, torch.empty_like(h), t, pos)
+    k = torch.zeros(4, 2, 16, 64, dtype=torch.int8)
+    s = torch.zeros(4, 2, 16)
+    with pytest.raises(TypeError):
+        lcp.PagedKVCache(k.half(), k.half())
+    for a in ((k, k, None, s), (k, k, s, s.double()), (k, k[:2], s, s), (k.transpose(1, 2), k.transpose(1, 2), s, s)):
+        with pytest.raises(ValueError):
+            lcp.PagedKVCache(*a)
+    c = lcp.PagedKVCache(k, k.clone(), s, s.clone())
+    with pytest.raises(ValueError):
+        c.append(x, x[:2], pos)
+    with pytest.raises(ValueError):
+        c.append(x, x, pos.long())
+    with pytest.raises(ValueError):
+        c.append(x, x, pos, q=x)
+    with pytest.raises(ValueError):
+        c.read(pos, torch.empty(3, 2, 65), torch.empty(3, 2, 65))
+    pt, ln = torch.zeros(3, 2, dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
+    for a, kw in (((x.float(), pt, ln), {}), ((x, pt[:2], ln), {}), ((x, pt, ln.long()), {}),
+                  ((x, pt, ln), dict(out=torch.empty(3, 2, 32))), ((x, pt, ln), dict(lse=torch.empty(3, 2).double())),
+                  ((torch.zeros(3, 64, 2, dtype=bf).transpose(1, 2), pt, ln), {})):
+        with pytest.raises(ValueError):
+            c.attend(*a, **kw)
+    with pytest.raises(lcp.LcpError):       # heads of q not a multiple of the cache's
+        c.attend(torch.zeros(3, 3, 64, dtype=bf), pt, ln)
