@@ -51,7 +51,7 @@ int check_cache(const lcp_kv_cache* c, KvCache* out) {
 int check_attn_sizes(const lcp_kv_cache* c, int B, int hq, int max_len, int window) {
   if (B <= 0 || hq <= 0 || max_len < 0 || window < 0) return LCP_E_INVAL;
   if (hq % c->heads != 0) return LCP_E_INVAL;
-  if ((int64_t)B * hq * c->D >= ((int64_t)1 << 31) || max_len >= (1 << 30)) return LCP_E_INVAL;
+  if ((int64_t)B * hq * c->D >= ((int64_t)1 << 31) || max_len >= (1 << 28)) return LCP_E_INVAL;
   return LCP_OK;
 }
 
