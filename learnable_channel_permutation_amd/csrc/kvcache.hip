@@ -7,7 +7,6 @@ namespace {
 
 // fp32 -> one e4m3 code (nearest even); |v| <= 448 or NaN
 __device__ __forceinline__ uint32_t to_e4m3(float v) { return __builtin_amdgcn_cvt_pk_fp8_f32(v, v, 0, false) & 0xff; }
-__device__ __forceinline__ float from_e4m3(uint32_t c) { return __builtin_amdgcn_cvt_f32_fp8((int)c, 0); }
 
 // The rotation with two rounded products and one rounded sum, never a fused
 // multiply-add: the 8-bit codes then follow from the definition in fp32 to the
@@ -32,7 +31,8 @@ __device__ __forceinline__ float row_scale(uint32_t a, int format) {
   return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
-// One wave per (token, head row): lane l holds channels l, l + 64, ..
+// Rows that are not 16-byte aligned: one wave per (token, head row), lane l
+// holds channels l, l + 64, .. and loads element by element.
 __global__ __launch_bounds__(64) void kv_append_rows_kernel(KvAppendArgs a) {
   const int lane = threadIdx.x, rows = a.q.heads + 2 * a.c.heads;
   const int64_t id = blockIdx.x;
@@ -88,44 +88,257 @@ __global__ __launch_bounds__(64) void kv_append_rows_kernel(KvAppendArgs a) {
   if (lane == 0) (which == 1 ? a.c.ks : a.c.vs)[row] = s;
 }
 
-// One thread per element.
-__global__ void kv_read_kernel(KvCache c, const int* slots, int64_t n, void* k, void* v, int bf16) {
-  const int64_t id = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (id >= 2 * n) return;
-  const bool isv = id >= n;
-  const int64_t i = isv ? id - n : id;
-  const int d = (int)(i % c.D);
-  const int64_t th = i / c.D;
-  const int h = (int)(th % c.heads), slot = slots[th / c.heads];
-  float x = 0.f;
-  if (slot >= 0 && slot < c.pages * c.ps) {
-    const int64_t row = ((int64_t)(slot / c.ps) * c.heads + h) * c.ps + slot % c.ps;
-    const void* src = isv ? c.v : c.k;
-    if (c.format == KV_BF16) {
-      x = bf2f(((const uint16_t*)src)[row * c.D + d]);
+// x / s rounded to the nearest fp32, with inv the rounded 1 / s: a product, its
+// exact remainder and one correction (Markstein), while s is large enough for
+// the remainder to be exact.
+__device__ __forceinline__ float divided(float x, float s, float inv) {
+  const float q = x * inv;
+  return fmaf(fmaf(-q, s, x), inv, q);
+}
+
+// Largest magnitude (as bits) over the L adjacent lanes that hold a row.
+template <int L>
+__device__ __forceinline__ uint32_t row_top(uint32_t v) {
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xf, 0xf, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xf, 0xf, false));
+  if (L >= 8) v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xf, 0xf, false));
+  if (L >= 16) v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xf, 0xf, false));
+  return v;
+}
+
+// Eight fp32 numbers -> eight codes.
+template <int FMT>
+__device__ __forceinline__ uint2 encode8(const float* f, float s, float inv) {
+  uint2 w;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    float y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (FMT == KV_E4M3) y[i] = f[4 * j + i] * inv;           // a power of two: exact
+      else y[i] = s < 0x1p-100f ? f[4 * j + i] / s : divided(f[4 * j + i], s, inv);
+    }
+    if (FMT == KV_E4M3) {
+      uint32_t r = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
+      r = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], (int)r, true);
+      (j ? w.y : w.x) = r;
     } else {
-      const uint8_t code = ((const uint8_t*)src)[row * c.D + d];
-      x = c.format == KV_E4M3 ? from_e4m3(code) : (float)(int8_t)code;
-      x *= (isv ? c.vs : c.ks)[row];
+      uint32_t r = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        r |= ((uint32_t)(int)fminf(fmaxf(rintf(y[i]), -127.f), 127.f) & 0xffu) << (8 * i);
+      (j ? w.y : w.x) = r;
     }
   }
-  void* dst = isv ? v : k;
-  if (bf16) ((uint16_t*)dst)[i] = (uint16_t)f2bf(x);
-  else ((float*)dst)[i] = x;
+  return w;
+}
+
+// Items: (token, group of heads, unit). A unit is 16 channels of a head row:
+// two chunks of 8, a rotary pair's halves or neighbours; the D / 16 units of a
+// row are adjacent lanes, which find its maximum among themselves. A thread
+// handles the same unit of N heads with one read of the table. Groups come as
+// those of q, of k, of v.
+struct AppendItems {
+  int gq, gkv;           // groups of N heads of q, and of k (and of v)
+  int64_t n;
+};
+
+template <int FMT, int D, int N>
+__global__ __launch_bounds__(256) void kv_append_kernel(KvAppendArgs a, AppendItems it) {
+  typedef RopeChunk<uint16_t, 8> C;
+  constexpr int U = D / 16;
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (id >= it.n) return;                      // n is a multiple of U: rows leave whole
+  const uint32_t per = (uint32_t)((it.gq + 2 * it.gkv) * U);
+  const int t = (int)(id / per);
+  const uint32_t in = (uint32_t)(id - (int64_t)t * per);
+  const int u = (int)(in % U);
+  int h = (int)(in / U);
+  const int which = h < it.gq ? 0 : h < it.gq + it.gkv ? 1 : 2;    // q, k, v
+  h -= which == 0 ? 0 : which == 1 ? it.gq : it.gq + it.gkv;
+  const Rows r = which == 0 ? a.q : which == 1 ? a.k : a.v;
+  const int step = which == 0 ? it.gq : it.gkv;
+  const bool turn = which != 2 && 16 * u < a.rot, split = turn && !a.interleaved;
+  const int d0 = split ? 8 * u : 16 * u, d1 = split ? d0 + a.rot / 2 : d0 + 8;
+  const uint16_t* x = (const uint16_t*)r.x + t * r.xt;
+  u32x4 w0[N], w1[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (h + i * step < r.heads) {
+      const uint16_t* xi = x + (h + i * step) * r.xh;
+      w0[i] = *(const u32x4*)(xi + d0);
+      w1[i] = *(const u32x4*)(xi + d1);
+    }
+  float c[8], s[8];
+  if (turn) {
+    const int p = min(max(a.pos[t], 0), a.max_pos - 1);
+    const floatx4* tab = (const floatx4*)(a.table + (int64_t)p * (a.rot / 2) + 8 * u);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const floatx4 q = tab[j];
+      c[2 * j] = q[0]; c[2 * j + 1] = q[2];
+      s[2 * j] = q[1]; s[2 * j + 1] = q[3];
+    }
+  }
+  int64_t row = -1;
+  if (which != 0) {
+    const int slot = a.slots[t];
+    if (slot >= 0 && slot < a.c.pages * a.c.ps) {
+      const int page = slot / a.c.ps;
+      row = (int64_t)page * a.c.heads * a.c.ps + (slot - page * a.c.ps);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (h + i * step >= r.heads) break;
+    float f[16];
+    C::unpack(w0[i], f);
+    C::unpack(w1[i], f + 8);
+    if (turn) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float& y0 = f[a.interleaved ? 2 * j : j];
+        float& y1 = f[a.interleaved ? 2 * j + 1 : j + 8];
+        const float p = y0, q = y1;
+        y0 = rot_first(p, q, c[j], s[j]);
+        y1 = rot_second(p, q, c[j], s[j]);
+      }
+    }
+    if (which == 0) {
+      uint16_t* y = (uint16_t*)r.y + t * r.yt + (h + i * step) * r.yh;
+      *(u32x4*)(y + d0) = C::pack(f);
+      *(u32x4*)(y + d1) = C::pack(f + 8);
+      continue;
+    }
+    const int64_t at = row + (int64_t)(h + i * step) * a.c.ps;
+    char* dst = (char*)(which == 1 ? a.c.k : a.c.v);
+    if (FMT == KV_BF16) {
+      if (row >= 0) {
+        *(u32x4*)(dst + (at * D + d0) * 2) = C::pack(f);
+        *(u32x4*)(dst + (at * D + d1) * 2) = C::pack(f + 8);
+      }
+      continue;
+    }
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) top = max(top, __float_as_uint(f[j]) & 0x7fffffffu);
+    top = row_top<U>(top);
+    const float sc = row_scale(top, FMT), inv = 1.f / sc;
+    uint2 c0 = encode8<FMT>(f, sc, inv), c1 = encode8<FMT>(f + 8, sc, inv);
+    if (top >= 0x7f800000u) c0 = c1 = make_uint2(0u, 0u);
+    if (row >= 0) {
+      *(uint2*)(dst + at * D + d0) = c0;
+      *(uint2*)(dst + at * D + d1) = c1;
+      if (u == 0) (which == 1 ? a.c.ks : a.c.vs)[at] = sc;
+    }
+  }
+}
+
+// One thread per eight channels of a slot and head, K and V.
+template <int FMT, bool BF>
+__global__ __launch_bounds__(256) void kv_read_kernel(KvCache c, const int* slots, int64_t n, char* ko, char* vo) {
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (id >= n) return;
+  const uint32_t U = c.D / 8, per = U * c.heads;
+  const int t = (int)(id / per);
+  const uint32_t in = (uint32_t)(id - (int64_t)t * per);
+  const int d = (int)(in % U) * 8, h = (int)(in / U), slot = slots[t];
+  float f[2][8] = {};
+  if (slot >= 0 && slot < c.pages * c.ps) {
+    const int page = slot / c.ps;
+    const int64_t row = ((int64_t)page * c.heads + h) * c.ps + (slot - page * c.ps);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const char* src = (const char*)(i ? c.v : c.k);
+      if (FMT == KV_BF16) {
+        RopeChunk<uint16_t, 8>::unpack(*(const u32x4*)(src + (row * c.D + d) * 2), f[i]);
+      } else {
+        const uint2 w = *(const uint2*)(src + row * c.D + d);
+        const float s = (i ? c.vs : c.ks)[row];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int word = (int)(j < 4 ? w.x : w.y);
+          if (FMT == KV_INT8) f[i][j] = (float)(int8_t)(word >> (8 * (j & 3)));
+        }
+        if (FMT == KV_E4M3) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int word = (int)(j ? w.y : w.x);
+            const auto a = __builtin_amdgcn_cvt_pk_f32_fp8(word, false), b = __builtin_amdgcn_cvt_pk_f32_fp8(word, true);
+            f[i][4 * j] = a[0]; f[i][4 * j + 1] = a[1]; f[i][4 * j + 2] = b[0]; f[i][4 * j + 3] = b[1];
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[i][j] *= s;
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    char* dst = i ? vo : ko;
+    if (BF) {
+      *(u32x4*)(dst + id * 16) = RopeChunk<uint16_t, 8>::pack(f[i]);
+    } else {
+      *(floatx4*)(dst + id * 32) = floatx4{f[i][0], f[i][1], f[i][2], f[i][3]};
+      *(floatx4*)(dst + id * 32 + 16) = floatx4{f[i][4], f[i][5], f[i][6], f[i][7]};
+    }
+  }
+}
+
+template <int FMT, int D, int N>
+hipError_t run_append(const KvAppendArgs& a, hipStream_t s) {
+  AppendItems it{};
+  it.gq = (a.q.heads + N - 1) / N;
+  it.gkv = (a.c.heads + N - 1) / N;
+  it.n = (int64_t)a.T * (it.gq + 2 * it.gkv) * (D / 16);
+  const int64_t grid = (it.n + 255) / 256;
+  if (grid > 0x7fffffff) return hipErrorInvalidValue;
+  kv_append_kernel<FMT, D, N><<<(unsigned)grid, 256, 0, s>>>(a, it);
+  return hipGetLastError();
+}
+
+template <int FMT, int D>
+hipError_t run_append_n(const KvAppendArgs& a, hipStream_t s) {
+  const int64_t items = (int64_t)a.T * (a.q.heads + 2 * a.c.heads) * (D / 16);
+  return items >= (int64_t)4 * 256 * 1024 ? run_append<FMT, D, 4>(a, s) : run_append<FMT, D, 1>(a, s);
+}
+
+template <int FMT>
+hipError_t run_append_d(const KvAppendArgs& a, hipStream_t s) {
+  if (a.c.D == 64) return run_append_n<FMT, 64>(a, s);
+  if (a.c.D == 128) return run_append_n<FMT, 128>(a, s);
+  return run_append_n<FMT, 256>(a, s);
+}
+
+template <int FMT>
+hipError_t run_read(const KvCache& c, const int* slots, int T, void* k, void* v, int bf16, hipStream_t s) {
+  const int64_t n = (int64_t)T * c.heads * (c.D / 8), grid = (n + 255) / 256;
+  if (grid > 0x7fffffff) return hipErrorInvalidValue;
+  if (bf16) kv_read_kernel<FMT, true><<<(unsigned)grid, 256, 0, s>>>(c, slots, n, (char*)k, (char*)v);
+  else kv_read_kernel<FMT, false><<<(unsigned)grid, 256, 0, s>>>(c, slots, n, (char*)k, (char*)v);
+  return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_kv_append(const KvAppendArgs& a, hipStream_t s) {
-  const int64_t rows = (int64_t)a.T * (a.q.heads + 2 * a.c.heads);
-  kv_append_rows_kernel<<<(unsigned)rows, 64, 0, s>>>(a);
-  return hipGetLastError();
+  const auto aligned = [](const Rows& r) {
+    return r.heads == 0 || ((((uintptr_t)r.x | (uintptr_t)r.y) & 15) == 0 && (r.xt | r.xh | r.yt | r.yh) % 8 == 0);
+  };
+  if (!aligned(a.q) || !aligned(a.k) || !aligned(a.v)) {
+    const int64_t rows = (int64_t)a.T * (a.q.heads + 2 * a.c.heads);
+    kv_append_rows_kernel<<<(unsigned)rows, 64, 0, s>>>(a);
+    return hipGetLastError();
+  }
+  if (a.c.format == KV_BF16) return run_append_d<KV_BF16>(a, s);
+  if (a.c.format == KV_E4M3) return run_append_d<KV_E4M3>(a, s);
+  return run_append_d<KV_INT8>(a, s);
 }
 
 hipError_t launch_kv_read(const KvCache& c, const int* slots, int T, void* k, void* v, int bf16, hipStream_t s) {
-  const int64_t n = (int64_t)T * c.heads * c.D;
-  kv_read_kernel<<<(unsigned)((2 * n + 255) / 256), 256, 0, s>>>(c, slots, n, k, v, bf16);
-  return hipGetLastError();
+  if (c.format == KV_BF16) return run_read<KV_BF16>(c, slots, T, k, v, bf16, s);
+  if (c.format == KV_E4M3) return run_read<KV_E4M3>(c, slots, T, k, v, bf16, s);
+  return run_read<KV_INT8>(c, slots, T, k, v, bf16, s);
 }
 
 }  // namespace lcp

@@ -12,6 +12,38 @@
 
 namespace lcp {
 
+// V adjacent elements of a row: the word that is loaded and stored, and its fp32 values.
+template <typename E, int V>
+struct RopeChunk;
+template <>
+struct RopeChunk<uint16_t, 8> {
+  typedef u32x4 T;
+  static __device__ __forceinline__ void unpack(T w, float* f) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) { f[2 * j] = lo_bf(w[j]); f[2 * j + 1] = hi_bf(w[j]); }
+  }
+  static __device__ __forceinline__ T pack(const float* f) {
+    return T{pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7])};
+  }
+};
+template <>
+struct RopeChunk<uint16_t, 4> {
+  typedef uint32_t T __attribute__((ext_vector_type(2)));
+  static __device__ __forceinline__ void unpack(T w, float* f) {
+    f[0] = lo_bf(w[0]); f[1] = hi_bf(w[0]); f[2] = lo_bf(w[1]); f[3] = hi_bf(w[1]);
+  }
+  static __device__ __forceinline__ T pack(const float* f) { return T{pack2(f[0], f[1]), pack2(f[2], f[3])}; }
+};
+template <>
+struct RopeChunk<float, 4> {
+  typedef floatx4 T;
+  static __device__ __forceinline__ void unpack(T w, float* f) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[j] = w[j];
+  }
+  static __device__ __forceinline__ T pack(const float* f) { return T{f[0], f[1], f[2], f[3]}; }
+};
+
 // Head rows [T][heads][D] with strides in elements, input and output.
 struct Rows {
   const void* x;

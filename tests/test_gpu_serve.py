@@ -227,6 +227,28 @@ def test_kv_append_and_read(T, hq, hk, D, ps, fmt, rot, interleaved):
             assert np.array_equal(down(got)[~bad], want.astype(np.float64)[~bad])
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "int8"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_kv_append_rows_of_any_alignment(fmt, D):
+    """Odd offsets and strides, head-major rows and broadcast values give the bits of aligned rows."""
+    say("kv append alignment", fmt, D)
+    T, hq, hk, ps = 21, 4, 2, 16
+    rows = {lay: [rope_case(T, h, D, lay, torch.bfloat16, 7 + i) for i, h in enumerate((hq, hk, hk))]
+            for lay in ("own", "odd", "head-major", "broadcast")}
+    table, pos = dev_f32(R.rope_table(64, R.rope_theta(D // 2))), dev_i32(np.arange(T))
+    slots = dev_i32(np.random.default_rng(1).permutation(3 * ps)[:T])
+    for lay, (q, k, v) in rows.items():
+        for inter in (False, True):
+            got = []
+            for a, b, c in ((q, k, v), [x.contiguous() for x in (q, k, v)]):
+                cache = new_cache(fmt, 3, ps, hk, D)
+                qo = torch.empty(T, hq, D, dtype=torch.bfloat16, device=DEV)
+                cache.append(b, c, slots, q=a, q_out=qo, table=table, pos=pos, interleaved=inter)
+                got.append([qo] + [x.view(torch.uint8) for x in (cache.k, cache.v, cache.k_scale, cache.v_scale)
+                                   if x is not None])
+            assert all(torch.equal(x, y) for x, y in zip(*got)), (lay, inter)
+
+
 def test_kv_offsets_beyond_32_bits():
     """Pages whose byte offset passes 2^32 (bf16: elements too), written, read and attended."""
     say("kv offsets beyond 32 bits")
