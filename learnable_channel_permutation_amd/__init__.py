@@ -169,11 +169,12 @@ class PagedKVCache:
         if max_len is None:
             max_len = pages.shape[1] * self.c.page_size
         if out is None:
-            out = _used_on(stream, torch.empty(q.shape, dtype=torch.bfloat16, device=q.device))
+            out = _used_on(stream, torch.empty_like(q, memory_format=torch.contiguous_format))
         if lse is None:
-            lse = _used_on(stream, torch.empty((B, hq), dtype=torch.float32, device=q.device))
+            lse = _used_on(stream, q.new_empty((B, hq), dtype=torch.float32))
         if ws is None:
             n = lcp_attn_decode_workspace_bytes(self.c, B, hq, max_len, window)
-            ws = _used_on(stream, torch.empty(n, dtype=torch.uint8, device=q.device))
+            if n:
+                ws = _used_on(stream, q.new_empty(n, dtype=torch.uint8))
         lcp_attn_decode(self.c, q, pages, lens, max_len, out, ws, lse, scale, window, stream)
         return out, lse

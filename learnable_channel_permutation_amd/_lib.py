@@ -153,6 +153,8 @@ def _load():
 
 LIB = _load()
 
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+
 
 def status_string(code):
     return LIB.lcp_status_string(int(code)).decode()
@@ -169,9 +171,11 @@ def _p(t):
 
 
 def _stream(stream=None):
+    """The HIP stream handle: the given stream's, or the current one of the current device (asked for by its raw
+    handle, which takes a twentieth of the time of building torch's stream object)."""
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+        return _raw_stream(_current_device())
+    return stream.cuda_stream
 
 
 def dtype_code(t):
@@ -358,33 +362,38 @@ def lcp_deploy_forward(vals, meta, perm, B, X, cout, Xp, Y, stream=None):
 
 # ---- serving operators --------------------------------------------------------
 _KV_FORMATS = {torch.bfloat16: LCP_KV_BF16, torch.float8_e4m3fn: LCP_KV_E4M3, torch.int8: LCP_KV_INT8}
+_I32, _BF16, _F32 = torch.int32, torch.bfloat16, torch.float32
 
 
-def _index(t, shape, name):
-    """A device int32 index array of the given shape."""
-    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError("%s must be contiguous int32 of shape %s" % (name, shape))
+def _index(t, n, name):
+    """A device int32 index array of n entries."""
+    if t.dtype is not _I32 or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError("%s must be contiguous int32 of shape (%d,)" % (name, n))
     return t.data_ptr()
 
 
 def _heads(x, y, D, dtype, name):
     """Head rows [T, heads, D] (any strides, channels contiguous)."""
-    if x.dim() != 3 or x.shape[2] != D or x.stride(2) != 1 or x.dtype != dtype:
-        raise ValueError("%s must be [T, heads, %d] %s with contiguous channels" % (name, D, dtype))
-    st, sh, _ = x.stride()
+    shape = x.shape
+    if len(shape) != 3 or shape[2] != D or x.dtype is not dtype:
+        raise ValueError("%s must be [T, heads, %d] %s" % (name, D, dtype))
+    st, sh, sd = x.stride()
+    if sd != 1:
+        raise ValueError("%s must have contiguous channels" % name)
     if y is None:
-        return lcp_heads(x.data_ptr(), None, x.shape[1], st, sh, 0, 0)
-    if y.shape != x.shape or y.stride(2) != 1 or y.dtype != dtype:
+        return lcp_heads(x.data_ptr(), None, shape[1], st, sh, 0, 0)
+    if y.shape != shape or y.dtype is not dtype or y.stride(2) != 1:
         raise ValueError("the output of %s must have its shape and dtype and contiguous channels" % name)
     yt, yh, _ = y.stride()
-    return lcp_heads(x.data_ptr(), y.data_ptr(), x.shape[1], st, sh, yt, yh)
+    return lcp_heads(x.data_ptr(), y.data_ptr(), shape[1], st, sh, yt, yh)
 
 
 def _table(table):
     """A rotary table [max_pos, rot_dim / 2, 2] -> (pointer, max_pos, rot_dim)."""
-    if table.dim() != 3 or table.shape[2] != 2 or table.dtype != torch.float32 or not table.is_contiguous():
+    shape = table.shape
+    if len(shape) != 3 or shape[2] != 2 or table.dtype is not _F32 or not table.is_contiguous():
         raise ValueError("table must be contiguous float32 [max_pos, rot_dim / 2, 2]")
-    return table.data_ptr(), table.shape[0], 2 * table.shape[1]
+    return table.data_ptr(), shape[0], 2 * shape[1]
 
 
 def make_rope_cfg(rot_dim, base=10000.0, scaling="none", factor=1.0, orig_len=0.0, low_turns=1.0, high_turns=32.0,
@@ -403,81 +412,93 @@ def lcp_rope_table(cfg, table, stream=None):
 
 def lcp_rope(q, q_out, table, pos, k=None, k_out=None, interleaved=False, inverse=False, stream=None):
     T, _, D = q.shape
-    hq = _heads(q, q_out, D, q.dtype, "q")
+    dtype = q.dtype
+    hq = _heads(q, q_out, D, dtype, "q")
     hk = None
     if k is not None:
         if k.shape[0] != T or k_out is None:
             raise ValueError("k needs q's number of tokens and an output")
-        hk = ctypes.byref(_heads(k, k_out, D, q.dtype, "k"))
+        hk = ctypes.byref(_heads(k, k_out, D, dtype, "k"))
     p, max_pos, rot = _table(table)
-    return _check("lcp_rope", LIB.lcp_rope(ctypes.byref(hq), hk, dtype_code(q), T, D, p, max_pos,
-                                           _index(pos, (T,), "pos"), rot, 1 if interleaved else 0, 1 if inverse else 0,
-                                           _stream(stream)))
+    code = LIB.lcp_rope(ctypes.byref(hq), hk, dtype_code(q), T, D, p, max_pos, _index(pos, T, "pos"), rot,
+                        1 if interleaved else 0, 1 if inverse else 0, _stream(stream))
+    return _check("lcp_rope", code)
 
 
 def make_kv_cache(k, v, k_scale=None, v_scale=None):
     """lcp_kv_cache over pages [pages, heads, page_size, D] (bfloat16, float8_e4m3fn or int8) and, for the 8-bit
     formats, scales [pages, heads, page_size]."""
-    if k.dtype not in _KV_FORMATS:
-        raise TypeError("unsupported cache dtype %s" % k.dtype)
-    if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or not (k.is_contiguous() and v.is_contiguous()):
+    dtype, shape = k.dtype, k.shape
+    fmt = _KV_FORMATS.get(dtype)
+    if fmt is None:
+        raise TypeError("unsupported cache dtype %s" % dtype)
+    if len(shape) != 4 or shape != v.shape or dtype is not v.dtype or not (k.is_contiguous() and v.is_contiguous()):
         raise ValueError("k and v must be contiguous [pages, heads, page_size, D] of one dtype")
-    pages, heads, ps, D = k.shape
     sk = sv = None
-    if k.dtype != torch.bfloat16:
+    if fmt != LCP_KV_BF16:
         if k_scale is None or v_scale is None:
             raise ValueError("8-bit caches need k_scale and v_scale")
         for s in (k_scale, v_scale):
-            if s.dtype != torch.float32 or tuple(s.shape) != (pages, heads, ps) or not s.is_contiguous():
+            if s.dtype is not _F32 or s.shape != shape[:3] or not s.is_contiguous():
                 raise ValueError("scales must be contiguous float32 [pages, heads, page_size]")
         sk, sv = k_scale.data_ptr(), v_scale.data_ptr()
-    return lcp_kv_cache(k.data_ptr(), v.data_ptr(), sk, sv, _KV_FORMATS[k.dtype], pages, ps, heads, D)
+    pages, heads, ps, D = shape
+    return lcp_kv_cache(k.data_ptr(), v.data_ptr(), sk, sv, fmt, pages, ps, heads, D)
 
 
 def lcp_kv_append(cache, k, v, slots, q=None, q_out=None, table=None, pos=None, interleaved=False, stream=None):
-    T = k.shape[0]
-    hk, hv = _heads(k, None, cache.D, torch.bfloat16, "k"), _heads(v, None, cache.D, torch.bfloat16, "v")
-    if v.shape[0] != T or (q is not None and (q.shape[0] != T or q_out is None or table is None)):
-        raise ValueError("q, k and v need one number of tokens, and q an output and a table")
-    hq = None if q is None else ctypes.byref(_heads(q, q_out, cache.D, torch.bfloat16, "q"))
-    p, max_pos, rot = (None, 0, 0) if table is None else _table(table)
-    pp = None if table is None else _index(pos, (T,), "pos")
-    return _check("lcp_kv_append", LIB.lcp_kv_append(ctypes.byref(cache), hq, ctypes.byref(hk), ctypes.byref(hv), T,
-                                                     _index(slots, (T,), "slots"), p, max_pos, pp, rot,
-                                                     1 if interleaved else 0, _stream(stream)))
+    T, D = k.shape[0], cache.D
+    hk, hv = _heads(k, None, D, _BF16, "k"), _heads(v, None, D, _BF16, "v")
+    if v.shape[0] != T:
+        raise ValueError("k and v need one number of tokens")
+    hq = None
+    if q is not None:
+        if q.shape[0] != T or q_out is None or table is None:
+            raise ValueError("q needs k's number of tokens, an output and a table")
+        hq = ctypes.byref(_heads(q, q_out, D, _BF16, "q"))
+    p = pp = None
+    max_pos = rot = 0
+    if table is not None:
+        p, max_pos, rot = _table(table)
+        pp = _index(pos, T, "pos")
+    code = LIB.lcp_kv_append(ctypes.byref(cache), hq, ctypes.byref(hk), ctypes.byref(hv), T, _index(slots, T, "slots"),
+                             p, max_pos, pp, rot, 1 if interleaved else 0, _stream(stream))
+    return _check("lcp_kv_append", code)
 
 
 def lcp_kv_read(cache, slots, k_out, v_out, stream=None):
     T = slots.shape[0]
-    for x in (k_out, v_out):
-        if tuple(x.shape) != (T, cache.heads, cache.D) or x.dtype != k_out.dtype or not x.is_contiguous():
-            raise ValueError("k_out and v_out must be contiguous [T, heads, D] of one dtype")
-    return _check("lcp_kv_read", LIB.lcp_kv_read(ctypes.byref(cache), _index(slots, (T,), "slots"), T,
-                                                 k_out.data_ptr(), v_out.data_ptr(), dtype_code(k_out),
-                                                 _stream(stream)))
+    shape = (T, cache.heads, cache.D)
+    if k_out.shape != shape or v_out.shape != shape or v_out.dtype is not k_out.dtype or not (
+            k_out.is_contiguous() and v_out.is_contiguous()):
+        raise ValueError("k_out and v_out must be contiguous [T, heads, D] of one dtype")
+    code = LIB.lcp_kv_read(ctypes.byref(cache), _index(slots, T, "slots"), T, k_out.data_ptr(), v_out.data_ptr(),
+                           dtype_code(k_out), _stream(stream))
+    return _check("lcp_kv_read", code)
 
 
 def lcp_attn_decode_workspace_bytes(cache, B, hq, max_len, window=0):
     out = ctypes.c_size_t(0)
     _check("lcp_attn_decode_workspace_bytes",
-           LIB.lcp_attn_decode_workspace_bytes(ctypes.byref(cache), int(B), int(hq), int(max_len), int(window),
-                                               ctypes.byref(out)))
+           LIB.lcp_attn_decode_workspace_bytes(ctypes.byref(cache), B, hq, max_len, window, ctypes.byref(out)))
     return out.value
 
 
-def lcp_attn_decode(cache, q, pages, lens, max_len, out, ws, lse=None, scale=None, window=0, stream=None):
-    B, hq, D = q.shape
-    if q.dtype != torch.bfloat16 or D != cache.D or q.stride(2) != 1 or (hq > 1 and q.stride(1) != D):
+def lcp_attn_decode(cache, q, pages, lens, max_len, out, ws=None, lse=None, scale=None, window=0, stream=None):
+    """ws: a uint8 tensor of lcp_attn_decode_workspace_bytes bytes, or None where that says 0."""
+    shape = q.shape
+    B, hq, D = shape
+    row, head, one = q.stride()
+    if q.dtype is not _BF16 or D != cache.D or one != 1 or (hq > 1 and head != D):
         raise ValueError("q must be [B, heads, %d] bfloat16 with adjacent heads" % cache.D)
-    if out.shape != q.shape or not out.is_contiguous():
+    if out.shape != shape or not out.is_contiguous():
         raise ValueError("out must be contiguous and have q's shape")
-    if lse is not None and (tuple(lse.shape) != (B, hq) or lse.dtype != torch.float32 or not lse.is_contiguous()):
+    if lse is not None and (lse.shape != (B, hq) or lse.dtype is not _F32 or not lse.is_contiguous()):
         raise ValueError("lse must be contiguous float32 [B, heads]")
-    row = q.stride(0) if B > 1 else hq * D
-    P = pages.shape[1]
-    return _check("lcp_attn_decode",
-                  LIB.lcp_attn_decode(ctypes.byref(cache), q.data_ptr(), row, B, hq, _index(pages, (B, P), "pages"), P,
-                                      _index(lens, (B,), "lens"), int(max_len), D ** -0.5 if scale is None else scale,
-                                      int(window), out.data_ptr(), dtype_code(out),
-                                      None if lse is None else lse.data_ptr(), ws.data_ptr(),
-                                      ws.numel() * ws.element_size(), _stream(stream)))
+    if pages.dim() != 2 or pages.shape[0] != B or pages.dtype is not _I32 or not pages.is_contiguous():
+        raise ValueError("pages must be contiguous int32 [B, max_pages]")
+    code = LIB.lcp_attn_decode(ctypes.byref(cache), q.data_ptr(), row if B > 1 else hq * D, B, hq, pages.data_ptr(),
+                               pages.shape[1], _index(lens, B, "lens"), max_len, D ** -0.5 if scale is None else scale,
+                               window, out.data_ptr(), dtype_code(out), None if lse is None else lse.data_ptr(),
+                               None if ws is None else ws.data_ptr(), 0 if ws is None else ws.nbytes, _stream(stream))
+    return _check("lcp_attn_decode", code)

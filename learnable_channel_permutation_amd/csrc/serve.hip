@@ -187,8 +187,9 @@ int lcp_attn_decode(const lcp_kv_cache* c, const void* q, int64_t q_row, int B, 
   if ((int64_t)B * max_pages >= ((int64_t)1 << 31)) return LCP_E_INVAL;
   if (q_row < (int64_t)hq * c->D || q_row > kMaxStride || q_row % 8 != 0) return LCP_E_INVAL;
   if (!aligned16(q) || !aligned16(out) || ((uintptr_t)lse & 3) != 0) return LCP_E_INVAL;
-  if (!ws || ((uintptr_t)ws & 255) != 0) return ws ? LCP_E_WORKSPACE : LCP_E_INVAL;
-  if (ws_bytes < attn_workspace_bytes(a.c, B, hq, max_len, window)) return LCP_E_WORKSPACE;
+  const size_t need = attn_workspace_bytes(a.c, B, hq, max_len, window);
+  if (need > 0 && !ws) return LCP_E_INVAL;
+  if (need > 0 && (((uintptr_t)ws & 255) != 0 || ws_bytes < need)) return LCP_E_WORKSPACE;
   a.q = (const uint16_t*)q;
   a.qrow = q_row;
   a.B = B;

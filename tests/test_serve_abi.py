@@ -115,15 +115,15 @@ def test_attend_refusals():
 
     for bad in (dict(q=None), dict(q=P + 8), dict(row=504), dict(row=516), dict(B=0), dict(hq=0), dict(hq=6),
                 dict(pages=None), dict(mp=0), dict(lens=None), dict(ml=-1), dict(ml=161), dict(scale=math.nan),
-                dict(scale=math.inf), dict(window=-1), dict(out=None), dict(out=P + 4), dict(lse=P + 2), dict(ws=None),
-                dict(B=1 << 23)):
+                dict(scale=math.inf), dict(window=-1), dict(out=None), dict(out=P + 4), dict(lse=P + 2),
+                dict(B=1 << 23), dict(ml=16000, mp=1000, ws=None)):
         assert call(**bad) == L.LCP_E_INVAL, bad
     assert call(odt=4) == L.LCP_E_UNSUPPORTED
-    assert call(ws=P + 128) == L.LCP_E_WORKSPACE
-    assert call(n=0) == L.LCP_E_WORKSPACE
     c = _cache(L)
-    need = L.lcp_attn_decode_workspace_bytes(c, 2, 4, 160)
-    assert need > 0 and call(ml=160, n=need - 1) == L.LCP_E_WORKSPACE
+    need = L.lcp_attn_decode_workspace_bytes(c, 2, 4, 16000)       # long enough to be split
+    assert need > 0 and need % 256 == 0
+    for bad in (dict(ws=P + 128), dict(n=0), dict(n=need - 1)):
+        assert call(ml=16000, mp=1000, **bad) == L.LCP_E_WORKSPACE, bad
     with pytest.raises(L.LcpError) as e:
         L.lcp_attn_decode_workspace_bytes(c, 0, 4, 160)
     assert e.value.code == L.LCP_E_INVAL
