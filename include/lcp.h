@@ -515,7 +515,7 @@ int lcp_kv_read(const lcp_kv_cache* c, const int32_t* slots, int T, void* k_out,
  *   q: bf16 [B][hq][D] with q_row elements between sequences (>= hq D), heads
  *   adjacent, 16-byte aligned rows; hq a multiple of heads.
  *   pages: [B][max_pages], the page number of tokens page_size i ..; entries
- *   that no counted token needs are not read; tokens of a page number outside
+ *   that no counted token needs have no effect; tokens of a page number outside
  *   the cache are left out. lens[b] is held to [0, max_len]; max_len <= max_pages
  *   page_size is the caller's bound, from which the split is chosen.
  *   out: [B][hq][D] in odt (F32 or BF16), 16-byte aligned; lse (nullable):

@@ -21,6 +21,8 @@
 //     (h, g) supplies K slots 8g .. 8g+7, which are the tokens named above. So
 //     lane (c, g) loads those eight tokens' channels c D/16 .. of V, and the
 //     transposition is a byte permutation within the lane.
+#include <algorithm>
+
 #include "serve.h"
 
 namespace lcp {
@@ -34,6 +36,7 @@ constexpr float kLowest = -3.402823466e38f;  // running maximum before any token
 constexpr float kLazy = 8.f;                 // the maximum follows once a score passes it by this (in log2)
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a), as_bf16x8(b), c, 0, 0, 0);
@@ -48,13 +51,103 @@ __device__ __forceinline__ uint32_t codes2(uint32_t w) {
   return pack2_exact((float)c0, (float)c1);
 }
 
-struct Plan {            // the same for every workgroup
-  int chunk, nch;        // tokens of a chunk (a multiple of kRound), chunks a sequence can have
+// How the work is dealt. A unit is one sequence, one key/value head and up to 16
+// of its query heads; its work is counted in steps.
+//   direct (wgs == 0): a workgroup a unit, no second kernel. Where no sequence
+//     can have more than kDirect steps.
+//   else: the steps of all units in a row, each unit led by kExtra steps that
+//     stand for what beginning and ending it costs, cut into parts that differ
+//     by one step at most, whatever the sequences' lengths are. A workgroup finds
+//     its part from the lengths and writes a unit that it holds whole to the
+//     output, a unit's piece to the workspace: at most two, in its places 0 (its
+//     first unit) and 1 (its last). The second kernel joins the pieces of each
+//     unit in order.
+struct Plan {
+  int wgs;
   int G, ht;             // query heads of a group, head tiles of 16 in it
+  int units;             // units of a sequence: heads * ht
+  int nh;                // query heads of a unit (the last tile may have fewer)
   uint32_t tpm;          // ceil(2^32 / (page_size / 16)): page of a 16-token tile by a high product
-  float* part;           // partial sums [B * hq][nch][D], then maxima and sums [B * hq][nch][2]
-  float2* ml;
+  float* part;           // [2 wgs][nh][D]
+  float2* ml;            // [2 wgs][nh] maximum and sum
 };
+constexpr int kDirect = 16;
+constexpr uint32_t kLeast = 16;     // steps of a part, where there are fewer than wgs such parts
+constexpr int kExtra = 8;
+
+// The cut of `all` steps.
+struct Cut {
+  uint32_t parts, q, r;        // the first r parts have q + 1 steps, the others q
+  __device__ __forceinline__ Cut(uint32_t all, uint32_t wgs) {
+    parts = min(wgs, max(1u, all / kLeast));
+    q = all / parts;
+    r = all - q * parts;
+  }
+  __device__ __forceinline__ uint32_t start(uint32_t i) const { return i * q + min(i, r); }
+  __device__ __forceinline__ uint32_t part_of(uint32_t x) const {
+    const uint32_t big = r * (q + 1);
+    return x < big ? x / (q + 1) : r + (x - big) / q;
+  }
+};
+
+// An index array entry at an address that is the same for the whole wave, read
+// through the scalar cache (the arrays are inputs, which no kernel writes): it
+// does not queue behind the loads of K and V, which return in order.
+__device__ __forceinline__ int uniform(const int* p, int64_t i) {
+  typedef const int __attribute__((address_space(4))) * ConstPtr;
+  return ((ConstPtr)(uintptr_t)p)[i];
+}
+
+// A store that the compiler knows to be to global memory. Through a pointer it
+// cannot place it makes flat stores, whose completion is out of order with the
+// loads: every wait in the kernel then becomes one for all of them.
+template <typename T>
+__device__ __forceinline__ void put(void* p, int64_t i, T v) {
+  typedef T __attribute__((address_space(1))) * GlobalPtr;
+  ((GlobalPtr)(uintptr_t)p)[i] = v;
+}
+__device__ __forceinline__ void put_out(const AttnArgs& a, int64_t i, float v) {
+  if (a.out_bf16) put<uint16_t>(a.out, i, (uint16_t)f2bf(v));
+  else put<float>(a.out, i, v);
+}
+// The log-sum-exp of a row from its maximum and sum in base 2.
+__device__ __forceinline__ void put_lse(const AttnArgs& a, int64_t row, float m, float l) {
+  if (a.lse) put<float>(a.lse, row, l == 0.f ? -__builtin_inff() : (m + log2_(l)) * 0.6931471805599453f);
+}
+
+// Tokens of a sequence: the first counted one, the end, and the steps between.
+struct Span {
+  int lo, end, steps;
+  __device__ __forceinline__ uint32_t cost() const { return steps ? steps + kExtra : 0; }
+};
+__device__ __forceinline__ Span span_of(const AttnArgs& a, int len) {
+  Span s;
+  s.end = min(max(len, 0), a.max_len);
+  s.lo = a.window && s.end > a.window ? s.end - a.window : 0;
+  s.steps = (s.end - (s.lo & ~(kStep - 1)) + kStep - 1) / kStep;
+  return s;
+}
+
+// Cost (of one unit) of the sequences before each thread's first, threadIdx.x *
+// per, and of all, by the 256 threads of a workgroup.
+__device__ __forceinline__ uint32_t cost_before(const AttnArgs& a, int per, uint32_t* total, uint32_t* lds) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  uint32_t mine = 0;
+  for (int i = 0; i < per; ++i) {
+    const int b = threadIdx.x * per + i;
+    if (b < a.B) mine += span_of(a, a.lens[b]).cost();
+  }
+  uint32_t sum = mine;
+  for (int k = 1; k < 64; k <<= 1) {
+    const uint32_t v = __shfl_up(sum, k, 64);
+    if (lane >= k) sum += v;
+  }
+  if (lane == 63) lds[wave] = sum;
+  __syncthreads();
+  *total = __builtin_amdgcn_readfirstlane(lds[0] + lds[1] + lds[2] + lds[3]);
+  for (int w = 0; w < wave; ++w) sum += lds[w];
+  return sum - mine;
+}
 
 // A half step: 16 tokens, all of one page.
 struct Half {
@@ -62,8 +155,15 @@ struct Half {
   int ok;                // whether the page exists and the half begins before the end
 };
 
-template <int FMT, int D>
-__global__ __launch_bounds__(256) void attn_chunk_kernel(AttnArgs a, Plan p) {
+template <typename T>
+__device__ __forceinline__ T once(const void* p) { return __builtin_nontemporal_load((const T*)p); }
+
+// Waves per SIMD that the registers leave (checked by the compiler): what
+// hides the loads' latency, and the number of workgroups that run at a time.
+constexpr int waves_for(int D) { return D == 64 ? 4 : D == 128 ? 3 : 2; }
+
+template <int FMT, int D, bool DEALT>
+__global__ __launch_bounds__(256, waves_for(D)) void attn_units_kernel(AttnArgs a, Plan p) {
   constexpr int E = FMT == KV_BF16 ? 2 : 1;
   constexpr int KL = D * E / 64;               // 16-byte K loads of a lane for 16 tokens
   constexpr int VC = D / 16;                   // channels of V a lane holds of each of its 8 tokens
@@ -72,45 +172,67 @@ __global__ __launch_bounds__(256) void attn_chunk_kernel(AttnArgs a, Plan p) {
   constexpr int OS = D + 4;                    // row stride of the waves' sums in LDS
   __shared__ float so[kWaves][16][OS];
   __shared__ float sm[kWaves][16], sl[kWaves][16];
+  __shared__ uint32_t scan[kWaves + 2];
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c16 = lane & 15, g = lane >> 4;
-  const int units = a.c.heads * p.ht;
-  const int chunk_id = blockIdx.x / (a.B * units);
-  const int rest = blockIdx.x % (a.B * units);
-  const int b = rest / units, hk = rest % units / p.ht, h0 = rest % p.ht * 16;
-  const int len = min(max(a.lens[b], 0), a.max_len);
-  const int lo = a.window && len > a.window ? len - a.window : 0;
-  const int begin = (lo & ~(kStep - 1)) + chunk_id * p.chunk;
-  const int end = min(len, begin + p.chunk);
-  if (begin >= end && chunk_id > 0) return;    // chunk 0 of an empty sequence writes its zeros
-  const int nh = min(16, p.G - h0);
-  const int head0 = hk * p.G + h0;
 
-  // Q fragments: head c16, the channels that the K loads bring
-  u32x4 qf[QF];
-#pragma unroll
-  for (int m = 0; m < QF; ++m) {
-    const int d = E == 2 ? 32 * m + 8 * g : 64 * (m >> 1) + 16 * g + 8 * (m & 1);
-    qf[m] = u32x4{0, 0, 0, 0};
-    if (c16 < nh) qf[m] = *(const u32x4*)(a.q + b * a.qrow + (int64_t)(head0 + c16) * D + d);
+  // this workgroup's part: sequence b, unit u of it, from v of its cost on, `left`
+  // in all. What steers the loops has to be uniform for the compiler too: as lane
+  // values they cost 40 spilled registers (2 x 131071 int8: 150 us)
+  int b, u, v = 0, left = 1, place = 0;
+  if (DEALT) {
+    const int per = (a.B + 255) / 256;
+    uint32_t all;
+    uint32_t at = cost_before(a, per, &all, scan);
+    all *= p.units;
+    const Cut cut(all, p.wgs);
+    // neighbouring parts on one XCD (workgroups go to the eight in turn): head
+    // tiles of one key/value head then meet in its L2
+    const uint32_t run = (cut.parts + 7) >> 3, rank = (blockIdx.x & 7) * run + (blockIdx.x >> 3);
+    if ((blockIdx.x >> 3) >= run || rank >= cut.parts || all == 0) return;
+    const uint32_t x = cut.start(rank);
+    left = cut.start(rank + 1) - x;
+    place = 2 * rank;
+    for (int i = 0; i < per; ++i) {
+      const int bb = threadIdx.x * per + i;
+      if (bb >= a.B) break;
+      const uint32_t n = span_of(a, a.lens[bb]).cost();
+      if (at * p.units <= x && x < (at + n) * p.units) {
+        scan[kWaves] = bb;
+        scan[kWaves + 1] = x - at * p.units;
+      }
+      at += n;
+    }
+    __syncthreads();
+    b = __builtin_amdgcn_readfirstlane(scan[kWaves]);
+    const int in = __builtin_amdgcn_readfirstlane(scan[kWaves + 1]);
+    const int n = span_of(a, uniform(a.lens, b)).cost();
+    u = in / n;
+    v = in - u * n;
+  } else {
+    b = blockIdx.x / p.units;
+    u = blockIdx.x % p.units;
   }
 
-  const int* pages = a.pages + (int64_t)b * a.max_pages;
+  // the unit (or the piece of it) at work: its tokens from lo to end, this wave's
+  // next step t, its heads, and whether it is whole
+  int lo, end, t, hk, nh, head0, last;
+  bool whole;
+  const int* pages;
+  u32x4 qf[QF];
   const int tp = a.c.ps >> 4;
-  auto half_at = [&](int t) {                  // t: first token, a multiple of 16
+  // the page of the 16 tokens from t on (past the end: of the last ones), its
+  // number, and the cache row; row 0 stands in where there is nothing to read
+  auto page_at = [&](int t) {
+    const int tile = min(t >> 4, last);
+    return p.tpm == 0 ? tile : (int)__umulhi((uint32_t)tile, p.tpm);      // 0: one tile a page
+  };
+  auto half_at = [&](int t, int id) {
     Half r;
-    r.row = 0;
-    r.ok = 0;
-    if (t < end) {
-      const uint32_t tile = (uint32_t)t >> 4, pg = __umulhi(tile, p.tpm);
-      const uint32_t pgi = p.tpm == 0 ? tile : pg;      // one tile a page
-      const int id = __builtin_amdgcn_readfirstlane(pages[pgi]);
-      if (id >= 0 && id < a.c.pages) {
-        r.row = ((int64_t)id * a.c.heads + hk) * a.c.ps + (int)(tile - pgi * tp) * 16;
-        r.ok = 1;
-      }
-    }
+    r.ok = t < end && id >= 0 && id < a.c.pages;
+    const int64_t row = ((int64_t)id * a.c.heads + hk) * a.c.ps + (min(t >> 4, last) - page_at(t) * tp) * 16;
+    r.row = r.ok ? row : 0;
     return r;
   };
 
@@ -123,7 +245,7 @@ __global__ __launch_bounds__(256) void attn_chunk_kernel(AttnArgs a, Plan p) {
     for (int i = 0; i < 2; ++i) {
       const char* base = (const char*)a.c.k + hf[i].row * (D * E);
 #pragma unroll
-      for (int j = 0; j < KL; ++j) kf[i][j] = *(const u32x4*)(base + (koff + 64 * j));
+      for (int j = 0; j < KL; ++j) kf[i][j] = once<u32x4>(base + (koff + 64 * j));
       if (E == 1) ks[i] = *(const f32x4*)(a.c.ks + hf[i].row + 4 * g);
     }
   };
@@ -135,15 +257,15 @@ __global__ __launch_bounds__(256) void attn_chunk_kernel(AttnArgs a, Plan p) {
       for (int e = 0; e < 4; ++e) {
         const char* src = base + (voff + e * (D * E));
         uint32_t* dst = vw[4 * i + e];
-        if constexpr (VW == 1) dst[0] = *(const uint32_t*)src;
+        if constexpr (VW == 1) dst[0] = once<uint32_t>(src);
         if constexpr (VW == 2) {
-          const uint2 w = *(const uint2*)src;
-          dst[0] = w.x; dst[1] = w.y;
+          const u32x2 w = once<u32x2>(src);
+          dst[0] = w[0]; dst[1] = w[1];
         }
         if constexpr (VW >= 4) {
 #pragma unroll
           for (int j = 0; j < VW / 4; ++j) {
-            const u32x4 w = *(const u32x4*)(src + 16 * j);
+            const u32x4 w = once<u32x4>(src + 16 * j);
             dst[4 * j] = w[0]; dst[4 * j + 1] = w[1]; dst[4 * j + 2] = w[2]; dst[4 * j + 3] = w[3];
           }
         }
@@ -152,190 +274,296 @@ __global__ __launch_bounds__(256) void attn_chunk_kernel(AttnArgs a, Plan p) {
     }
   };
 
-  f32x4 o[VC];
-#pragma unroll
-  for (int j = 0; j < VC; ++j) o[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  float m = kLowest, l = 0.f;
-
-  int t = begin + wave * kStep;
+  // loads run a step ahead, page numbers two
   Half cur[2], nxt[2];
-  if (t < end) {
-    cur[0] = half_at(t);
-    cur[1] = half_at(t + 16);
+  int id0, id1;
+  // takes the unit at (b, u, v) up and issues its first loads; false if the part
+  // ends before its first step
+  auto begin_unit = [&]() {
+    if (left <= 0 || b >= a.B) return false;
+    const Span sp = span_of(a, uniform(a.lens, b));
+    int r0 = 0, r1 = sp.steps;
+    if (DEALT) {
+      r0 = max(0, v - kExtra);
+      r1 = min(r1, v + left - kExtra);
+      left -= sp.steps + kExtra - v;
+      v = 0;
+      if (r1 <= r0) return false;
+    } else {
+      left = 0;
+    }
+    whole = r0 == 0 && r1 == sp.steps;
+    hk = u / p.ht;
+    const int h0 = u % p.ht * 16;
+    nh = min(16, p.G - h0);
+    head0 = hk * p.G + h0;
+    lo = sp.lo;
+    const int begin = lo & ~(kStep - 1);
+    end = min(sp.end, begin + r1 * kStep);
+    last = max(end - 1, 0) >> 4;
+    t = begin + r0 * kStep + wave * kStep;
+    pages = a.pages + (int64_t)b * a.max_pages;
+    // Q fragments: head c16, the channels that the K loads bring
+#pragma unroll
+    for (int m = 0; m < QF; ++m) {
+      const int d = E == 2 ? 32 * m + 8 * g : 64 * (m >> 1) + 16 * g + 8 * (m & 1);
+      qf[m] = u32x4{0, 0, 0, 0};
+      if (c16 < nh) qf[m] = *(const u32x4*)(a.q + b * a.qrow + (int64_t)(head0 + c16) * D + d);
+    }
+    cur[0] = half_at(t, uniform(pages, page_at(t)));
+    cur[1] = half_at(t + 16, uniform(pages, page_at(t + 16)));
+    id0 = uniform(pages, page_at(t + kRound));
+    id1 = uniform(pages, page_at(t + kRound + 16));
+    // Q has come by the time the page numbers have; with this wait for it (vmcnt 0
+    // alone) the first product waits for K's loads only, not for V's behind them
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(0x0f70);
     load_k(cur);
+    __builtin_amdgcn_sched_barrier(0);         // K before V, for the same reason
     load_v(cur);
-  }
-  for (; t < end; t += kRound) {
-    const bool more = t + kRound < end;
-    if (more) {
-      nxt[0] = half_at(t + kRound);
-      nxt[1] = half_at(t + kRound + 16);
-    }
-    // scores of tokens 16 i + 4 g + e for head c16
-    f32x4 s[2];
+    __builtin_amdgcn_sched_barrier(0);
+    return true;
+  };
+
+  f32x4 o[VC];
+  float m = kLowest, l = 0.f;
+  bool done = false;                           // whether o, m and l hold a finished unit: the last one
+  int nh_ = 0, place_ = 0;
+  bool whole_ = false;
+  int64_t row0 = 0;
+  for (;;) {
+    // the next unit's first loads fly while the last one is joined and written
+    const bool more = begin_unit();
+    if (done) {
+      // join the waves: O^T tile j, register i of lane (h, g) is channel
+      // VC (4 g + i) + j of head h
+      l = xor32_sum(xor16_sum(l));
+      if (g == 0) { sm[wave][c16] = m; sl[wave][c16] = l; }
+      if (c16 < nh_) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      s[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int mm = 0; mm < QF; ++mm) {
-        u32x4 kk;
-        if constexpr (E == 2) {
-          kk = kf[i][mm];
-        } else {
-          const uint32_t w0 = kf[i][mm >> 1][2 * (mm & 1)], w1 = kf[i][mm >> 1][2 * (mm & 1) + 1];
-          kk = u32x4{codes2<FMT, false>(w0), codes2<FMT, true>(w0), codes2<FMT, false>(w1), codes2<FMT, true>(w1)};
-        }
-        s[i] = mfma16(kk, qf[mm], s[i]);
+          for (int j = 0; j < VC; j += 4)
+            *(f32x4*)&so[wave][c16][VC * (4 * g + i) + j] = f32x4{o[j][i], o[j + 1][i], o[j + 2][i], o[j + 3][i]};
       }
-      if (E == 1) s[i] *= ks[i] * a.scale2;
-      else s[i] *= a.scale2;
+      __syncthreads();
+      for (int idx = threadIdx.x; idx < nh_ * D; idx += 256) {
+        const int h = idx / D, d = idx % D;
+        float M = sm[0][h];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) M = fmaxf(M, sm[w][h]);
+        float L = 0.f, y = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+          const float r = exp2_(sm[w][h] - M);
+          L += sl[w][h] * r;
+          y += so[w][h][d] * r;
+        }
+        if (!whole_) {
+          const int at = place_ * p.nh + h;
+          put<float>(p.part, (int64_t)at * D + d, y);
+          if (d == 0) put<u32x2>(p.ml, at, u32x2{__float_as_uint(M), __float_as_uint(L)});
+          continue;
+        }
+        const int64_t row = row0 + h;
+        put_out(a, row * D + d, L == 0.f ? 0.f : y / L);
+        if (d == 0) put_lse(a, row, M, L);
+      }
+      if (!more) return;
+      __syncthreads();                         // the sums in LDS have been read
     }
-    f32x4 vsc[2];
-    if (E == 1) { vsc[0] = vs[0]; vsc[1] = vs[1]; }
-    const bool full = cur[0].ok && cur[1].ok && t >= lo && t + kStep <= end;
-    if (!full) {
-      // what lies outside the counted tokens has no effect whatever its bits:
-      // scores -inf, V and its scale 0
+    if (!more) return;
+#pragma unroll
+    for (int j = 0; j < VC; ++j) o[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    m = kLowest;
+    l = 0.f;
+    for (; t < end; t += kRound) {
+      nxt[0] = half_at(t + kRound, id0);
+      nxt[1] = half_at(t + kRound + 16, id1);
+      id0 = uniform(pages, page_at(t + 2 * kRound));
+      id1 = uniform(pages, page_at(t + 2 * kRound + 16));
+      // scores of tokens 16 i + 4 g + e for head c16
+      f32x4 s[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        s[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int mm = 0; mm < QF; ++mm) {
+          u32x4 kk;
+          if constexpr (E == 2) {
+            kk = kf[i][mm];
+          } else {
+            const uint32_t w0 = kf[i][mm >> 1][2 * (mm & 1)], w1 = kf[i][mm >> 1][2 * (mm & 1) + 1];
+            kk = u32x4{codes2<FMT, false>(w0), codes2<FMT, true>(w0), codes2<FMT, false>(w1), codes2<FMT, true>(w1)};
+          }
+          s[i] = mfma16(kk, qf[mm], s[i]);
+        }
+        if (E == 1) s[i] *= ks[i] * a.scale2;
+        else s[i] *= a.scale2;
+      }
+      const bool full = cur[0].ok && cur[1].ok && t >= lo && t + kStep <= end;
+      if (!full) {
+        // what lies outside the counted tokens has no effect whatever its bits:
+        // scores -inf, V and its scale 0
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int tt = t + 16 * i + 4 * g + e;
+            const bool in = cur[i].ok && tt >= lo && tt < end;
+            s[i][e] = in ? s[i][e] : -__builtin_inff();
+            if (E == 1) vs[i][e] = in ? vs[i][e] : 0.f;
+#pragma unroll
+            for (int w = 0; w < VW; ++w) vw[4 * i + e][w] = in ? vw[4 * i + e][w] : 0u;
+          }
+      }
+      // the next step's K flies during the softmax and the products with V, its V
+      // during the next scores. Unconditional (past the end: row 0 of the cache),
+      // so that the waits can count on the loads in between
+      load_k(nxt);
+      __builtin_amdgcn_sched_barrier(0);
+      float top = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
+                        fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
+      if (__any(top > m + kLazy)) {
+        top = xor32_max(xor16_max(top));         // the head's four lanes agree on the maximum
+        const float mn = fmaxf(m, top), r = exp2_(m - mn);
+        m = mn;
+        l *= r;
+#pragma unroll
+        for (int j = 0; j < VC; ++j) o[j] *= r;
+      }
+      // p in two bfloat16 parts (their sum is p to 2^-16): the weights reach the
+      // sums with what fp32 arithmetic on them would keep
+      u32x4 ph, pl;
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int tt = t + 16 * i + 4 * g + e;
-          const bool in = cur[i].ok && tt >= lo && tt < end;
-          s[i][e] = in ? s[i][e] : -__builtin_inff();
-          if (E == 1) vsc[i][e] = in ? vsc[i][e] : 0.f;
-#pragma unroll
-          for (int w = 0; w < VW; ++w) vw[4 * i + e][w] = in ? vw[4 * i + e][w] : 0u;
+        for (int e = 0; e < 4; e += 2) {
+          float p0 = exp2_(s[i][e] - m), p1 = exp2_(s[i][e + 1] - m);
+          l += p0 + p1;
+          if (E == 1) { p0 *= vs[i][e]; p1 *= vs[i][e + 1]; }
+          const uint32_t hi = pack2(p0, p1);
+          ph[2 * i + e / 2] = hi;
+          pl[2 * i + e / 2] = pack2(p0 - lo_bf(hi), p1 - hi_bf(hi));
         }
-    }
-    if (more) load_k(nxt);
-    float top = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
-                      fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
-    if (__any(top > m + kLazy)) {
-      top = xor32_max(xor16_max(top));         // the head's four lanes agree on the maximum
-      const float mn = fmaxf(m, top), r = exp2_(m - mn);
-      m = mn;
-      l *= r;
 #pragma unroll
-      for (int j = 0; j < VC; ++j) o[j] *= r;
-    }
-    // p in two bfloat16 parts (their sum is p to 2^-16): the weights reach the
-    // sums with what fp32 arithmetic on them would keep
-    u32x4 ph, pl;
+      for (int j = 0; j < VC; ++j) {
+        u32x4 vv;
+        if constexpr (E == 2) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+          for (int w = 0; w < 4; ++w)
+            vv[w] = __builtin_amdgcn_perm(vw[2 * w + 1][j >> 1], vw[2 * w][j >> 1], j & 1 ? 0x07060302u : 0x05040100u);
+        } else {
 #pragma unroll
-      for (int e = 0; e < 4; e += 2) {
-        float p0 = exp2_(s[i][e] - m), p1 = exp2_(s[i][e + 1] - m);
-        l += p0 + p1;
-        if (E == 1) { p0 *= vsc[i][e]; p1 *= vsc[i][e + 1]; }
-        const uint32_t hi = pack2(p0, p1);
-        ph[2 * i + e / 2] = hi;
-        pl[2 * i + e / 2] = pack2(p0 - lo_bf(hi), p1 - hi_bf(hi));
-      }
-#pragma unroll
-    for (int j = 0; j < VC; ++j) {
-      u32x4 vv;
-      if constexpr (E == 2) {
-#pragma unroll
-        for (int w = 0; w < 4; ++w)
-          vv[w] = __builtin_amdgcn_perm(vw[2 * w + 1][j >> 1], vw[2 * w][j >> 1], j & 1 ? 0x07060302u : 0x05040100u);
-      } else {
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          // bytes j and j + 1 of both tokens; the odd channel uses the upper half
-          const uint32_t pr = __builtin_amdgcn_perm(vw[2 * w + 1][j >> 2], vw[2 * w][j >> 2],
-                                                    (j & 2) ? 0x07030602u : 0x05010400u);
-          vv[w] = j & 1 ? codes2<FMT, true>(pr) : codes2<FMT, false>(pr);
+          for (int w = 0; w < 4; ++w) {
+            // bytes j and j + 1 of both tokens; the odd channel uses the upper half
+            const uint32_t pr = __builtin_amdgcn_perm(vw[2 * w + 1][j >> 2], vw[2 * w][j >> 2],
+                                                      (j & 2) ? 0x07030602u : 0x05010400u);
+            vv[w] = j & 1 ? codes2<FMT, true>(pr) : codes2<FMT, false>(pr);
+          }
         }
+        o[j] = mfma16(vv, ph, o[j]);
+        o[j] = mfma16(vv, pl, o[j]);
       }
-      o[j] = mfma16(vv, ph, o[j]);
-      o[j] = mfma16(vv, pl, o[j]);
-    }
-    if (more) {
+      __builtin_amdgcn_sched_barrier(0);
       load_v(nxt);
       cur[0] = nxt[0];
       cur[1] = nxt[1];
     }
-  }
 
-  // join the waves: O^T tile j, register i of lane (h, g) is channel
-  // VC (4 g + i) + j of head h
-  l = xor32_sum(xor16_sum(l));
-  if (g == 0) { sm[wave][c16] = m; sl[wave][c16] = l; }
-  if (c16 < nh) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < VC; ++j) so[wave][c16][VC * (4 * g + i) + j] = o[j][i];
-  }
-  __syncthreads();
-  for (int idx = threadIdx.x; idx < nh * D; idx += 256) {
-    const int h = idx / D, d = idx % D;
-    float M = sm[0][h];
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w) M = fmaxf(M, sm[w][h]);
-    float L = 0.f, y = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      const float r = exp2_(sm[w][h] - M);
-      L += sl[w][h] * r;
-      y += so[w][h][d] * r;
+    done = true;
+    nh_ = nh;
+    place_ = place;
+    whole_ = whole;
+    row0 = (int64_t)b * a.hq + head0;
+    place |= 1;
+    if (DEALT && left > 0 && ++u == p.units) {
+      u = 0;
+      do ++b; while (b < a.B && span_of(a, uniform(a.lens, b)).steps == 0);
     }
-    const int64_t row = (int64_t)b * a.hq + head0 + h;
-    if (p.nch > 1) {
-      p.part[(row * p.nch + chunk_id) * D + d] = y;
-      if (d == 0) p.ml[row * p.nch + chunk_id] = make_float2(M, L);
-      continue;
-    }
-    y = L == 0.f ? 0.f : y / L;
-    if (a.out_bf16) ((uint16_t*)a.out)[row * D + d] = (uint16_t)f2bf(y);
-    else ((float*)a.out)[row * D + d] = y;
-    if (d == 0 && a.lse) a.lse[row] = L == 0.f ? -__builtin_inff() : (M + log2_(L)) * 0.6931471805599453f;
   }
 }
 
-// Joins the chunks of one query head: a workgroup per row, wave w takes chunks
-// w, w + 4, .. in order, then the waves in order.
-template <int D>
-__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, Plan p) {
-  constexpr int N = D / 64;
-  __shared__ float so[kWaves][D], sl[kWaves];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t row = blockIdx.x;
-  const int b = (int)(row / a.hq);
-  const int len = min(max(a.lens[b], 0), a.max_len);
-  const int lo = a.window && len > a.window ? len - a.window : 0;
-  const int n = max(1, (len - (lo & ~(kStep - 1)) + p.chunk - 1) / p.chunk);
-  const float2* ml = p.ml + row * p.nch;
-  const float* part = p.part + row * p.nch * D;
-  float M = kLowest;
-  for (int c = lane; c < n; c += 64) M = fmaxf(M, ml[c].x);
-  M = row16_max(M);
-  M = xor32_max(xor16_max(M));
-  float L = 0.f, y[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) y[i] = 0.f;
-  for (int c = wave; c < n; c += kWaves) {
-    const float2 v = ml[c];
-    const float r = exp2_(v.x - M);
-    L += v.y * r;
-#pragma unroll
-    for (int i = 0; i < N; ++i) y[i] += part[(int64_t)c * D + lane + 64 * i] * r;
+// Joins the pieces of the units that were cut, and answers for sequences
+// without tokens. D / 4 threads hold a head's channels, four each. ROWS: a
+// workgroup per query head, its thread groups share the pieces (few units of
+// many pieces); else a sequence's units go over `groups` workgroups, a thread
+// group takes a head at a time.
+template <int D, bool ROWS>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, Plan p, int groups) {
+  constexpr int TG = 256 / (D / 4);            // thread groups
+  __shared__ uint32_t scan[kWaves + 1];
+  __shared__ f32x4 so[TG][D / 4];
+  __shared__ float sm[TG], sl[TG];
+  const int b = (int)(blockIdx.x / groups), group = (int)(blockIdx.x % groups);
+  const int per = (a.B + 255) / 256;
+  uint32_t all;
+  uint32_t at = cost_before(a, per, &all, scan);
+  for (int i = 0; i < per; ++i) {
+    const int bb = threadIdx.x * per + i;
+    if (bb == b) scan[kWaves] = at;
+    if (bb < a.B) at += span_of(a, a.lens[bb]).cost();
   }
-  if (lane == 0) sl[wave] = L;
-#pragma unroll
-  for (int i = 0; i < N; ++i) so[wave][lane + 64 * i] = y[i];
   __syncthreads();
-  const int d = threadIdx.x;
-  if (d >= D) return;
-  float Z = 0.f, o = 0.f;
+  const uint32_t n = span_of(a, uniform(a.lens, b)).cost(), xb = scan[kWaves] * p.units;
+  const Cut cut(all * p.units, p.wgs);
+  const int tg = threadIdx.x / (D / 4), td = threadIdx.x % (D / 4);
+  for (int u = ROWS ? group / p.nh : group; u < p.units; u += ROWS ? p.units : groups) {
+  const uint32_t x0 = xb + u * n;
+  int w0 = 0, pieces = 0, place0 = 0;
+  if (n) {
+    w0 = cut.part_of(x0 + kExtra);             // the part of its first step
+    pieces = cut.part_of(x0 + n - 1) - w0 + 1;
+    if (pieces == 1) continue;                 // written whole by its workgroup
+    place0 = 2 * w0 + (x0 > cut.start(w0) ? 1 : 0);     // the first piece ends its workgroup's part
+  }
+  const int h0 = u % p.ht * 16, nh = min(16, p.G - h0);
+  for (int h = ROWS ? group % p.nh : tg; h < nh; h += ROWS ? nh : TG) {
+    float M = kLowest, L = 0.f;
+    f32x4 y = {0.f, 0.f, 0.f, 0.f};
+    for (int i = ROWS ? tg : 0; i < pieces; i += 4 * (ROWS ? TG : 1)) {
+      // four pieces' loads together, then one after the other
+      f32x4 v[4];
+      float2 ml[4];
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) { Z += sl[w]; o += so[w][d]; }
-  o = Z == 0.f ? 0.f : o / Z;
-  if (a.out_bf16) ((uint16_t*)a.out)[row * D + d] = (uint16_t)f2bf(o);
-  else ((float*)a.out)[row * D + d] = o;
-  if (d == 0 && a.lse) a.lse[row] = Z == 0.f ? -__builtin_inff() : (M + log2_(Z)) * 0.6931471805599453f;
+      for (int k = 0; k < 4; ++k) {
+        const int j = i + k * (ROWS ? TG : 1);
+        if (j < pieces) {
+          const int q = (j == 0 ? place0 : 2 * (w0 + j)) * p.nh + h;
+          ml[k] = p.ml[q];
+          v[k] = *(const f32x4*)(p.part + (int64_t)q * D + 4 * td);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (i + k * (ROWS ? TG : 1) < pieces) {
+          const float mn = fmaxf(M, ml[k].x), r0 = exp2_(M - mn), r1 = exp2_(ml[k].x - mn);
+          L = L * r0 + ml[k].y * r1;
+          y = y * r0 + v[k] * r1;
+          M = mn;
+        }
+      }
+    }
+    if (ROWS) {
+      so[tg][td] = y;
+      if (td == 0) { sm[tg] = M; sl[tg] = L; }
+      __syncthreads();
+      if (tg != 0) return;
+      for (int w = 1; w < TG; ++w) {
+        const float mn = fmaxf(M, sm[w]), r0 = exp2_(M - mn), r1 = exp2_(sm[w] - mn);
+        L = L * r0 + sl[w] * r1;
+        y = y * r0 + so[w][td] * r1;
+        M = mn;
+      }
+    }
+    const int64_t row = (int64_t)b * a.hq + u / p.ht * p.G + h0 + h;
+    if (L == 0.f) y = f32x4{0.f, 0.f, 0.f, 0.f};
+    else y /= L;
+    if (a.out_bf16) put<u32x2>(a.out, (row * D >> 2) + td, u32x2{pack2(y[0], y[1]), pack2(y[2], y[3])});
+    else put<f32x4>(a.out, (row * D >> 2) + td, y);
+    if (td == 0) put_lse(a, row, M, L);
+  }
+  }
 }
 
 inline size_t align256(size_t x) { return (x + 255) / 256 * 256; }
@@ -344,29 +572,36 @@ Plan make_plan(const KvCache& c, int B, int hq, int max_len, int window) {
   Plan p{};
   p.G = hq / c.heads;
   p.ht = (p.G + 15) / 16;
+  p.units = c.heads * p.ht;
+  p.nh = p.G < 16 ? p.G : 16;
   const int tp = c.ps / 16;
   p.tpm = tp == 1 ? 0u : (uint32_t)(((1ull << 32) + tp - 1) / tp);
   // the tokens a sequence can span: a window begins anywhere in a step
   int64_t span = max_len;
   if (window && window + (int64_t)kStep - 1 < span) span = window + (int64_t)kStep - 1;
-  const int64_t units = (int64_t)B * c.heads * p.ht;
-  const int64_t want = 2048;
-  int64_t chunk = (span * units / want + kRound - 1) / kRound * kRound;
-  if (chunk < 2 * kRound) chunk = 2 * kRound;
-  p.chunk = (int)chunk;
-  p.nch = (int)((span + chunk - 1) / chunk);
-  if (p.nch < 1) p.nch = 1;
+  if (span > kDirect * kStep) p.wgs = 256 * waves_for(c.D);
   return p;
 }
 
 template <int FMT, int D>
 hipError_t run(const AttnArgs& a, const Plan& p, hipStream_t s) {
-  const int64_t grid = (int64_t)a.B * a.c.heads * p.ht * p.nch;
-  if (grid > 0x7fffffff) return hipErrorInvalidValue;
-  attn_chunk_kernel<FMT, D><<<(unsigned)grid, 256, 0, s>>>(a, p);
+  const int64_t units = (int64_t)a.B * p.units;
+  if (units * p.nh > 0x7fffffff) return hipErrorInvalidValue;
+  if (p.wgs == 0) {
+    attn_units_kernel<FMT, D, false><<<(unsigned)units, 256, 0, s>>>(a, p);
+    return hipGetLastError();
+  }
+  attn_units_kernel<FMT, D, true><<<(unsigned)p.wgs, 256, 0, s>>>(a, p);
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || p.nch == 1) return e;
-  attn_join_kernel<D><<<(unsigned)(a.B * a.hq), 256, 0, s>>>(a, p);
+  if (e != hipSuccess) return e;
+  if (units * 8 <= p.wgs) {
+    const int groups = p.units * p.nh;         // eight pieces a unit and more
+    attn_join_kernel<D, true><<<(unsigned)(a.B * groups), 256, 0, s>>>(a, p, groups);
+  } else {
+    // every workgroup adds up all the lengths: the more sequences, the fewer groups
+    const int groups = std::min(p.units, std::max(1, 4096 / a.B));
+    attn_join_kernel<D, false><<<(unsigned)(a.B * groups), 256, 0, s>>>(a, p, groups);
+  }
   return hipGetLastError();
 }
 
@@ -381,15 +616,14 @@ hipError_t run_d(const AttnArgs& a, const Plan& p, hipStream_t s) {
 
 size_t attn_workspace_bytes(const KvCache& c, int B, int hq, int max_len, int window) {
   const Plan p = make_plan(c, B, hq, max_len, window);
-  if (p.nch == 1) return 0;
-  const size_t n = (size_t)B * hq * p.nch;
+  const size_t n = (size_t)2 * p.wgs * p.nh;
   return align256(n * c.D * 4) + align256(n * 8);
 }
 
 hipError_t launch_attn_decode(const AttnArgs& a, hipStream_t s) {
   Plan p = make_plan(a.c, a.B, a.hq, a.max_len, a.window);
   p.part = a.ws;
-  p.ml = (float2*)((char*)a.ws + align256((size_t)a.B * a.hq * p.nch * a.c.D * 4));
+  p.ml = (float2*)((char*)a.ws + align256((size_t)2 * p.wgs * p.nh * a.c.D * 4));
   if (a.c.format == KV_BF16) return run_d<KV_BF16>(a, p, s);
   if (a.c.format == KV_E4M3) return run_d<KV_E4M3>(a, p, s);
   return run_d<KV_INT8>(a, p, s);

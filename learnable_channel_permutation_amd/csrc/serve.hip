@@ -52,6 +52,9 @@ int check_attn_sizes(const lcp_kv_cache* c, int B, int hq, int max_len, int wind
   if (B <= 0 || hq <= 0 || max_len < 0 || window < 0) return LCP_E_INVAL;
   if (hq % c->heads != 0) return LCP_E_INVAL;
   if ((int64_t)B * hq * c->D >= ((int64_t)1 << 31) || max_len >= (1 << 28)) return LCP_E_INVAL;
+  // steps of 32 tokens over all sequences and head tiles in 32 bits
+  const int64_t units = (int64_t)B * c->heads * ((hq / c->heads + 15) / 16);
+  if (units * ((int64_t)max_len / 32 + 8) >= ((int64_t)1 << 31)) return LCP_E_INVAL;
   return LCP_OK;
 }
 

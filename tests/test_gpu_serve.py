@@ -386,6 +386,18 @@ def test_attend_long_other_heads(D):
     check_attend("int8", [6001, 0, 3], 17, 1, D, 16, window=5000)
 
 
+@pytest.mark.parametrize("B,n,hq,hk,D", [(300, 700, 2, 2, 64), (70, 1500, 16, 8, 64), (9, 4000, 34, 1, 64),
+                                          (530, 530, 1, 1, 64), (40, 1000, 32, 16, 64)])
+def test_attend_many_sequences(B, n, hq, hk, D):
+    """Batches whose rounds are dealt over the workgroups: units cut anywhere, several to a workgroup, empty ones among them."""
+    say("attend many", B, n, hq, hk, D)
+    rng = np.random.default_rng(B)
+    lens = rng.integers(0, n + 1, B)
+    lens[rng.integers(0, B, B // 5)] = 0
+    lens[rng.integers(0, B)] = n
+    check_attend("int8", [int(x) for x in lens], hq, hk, D, 32)
+
+
 def test_attend_empty_batch_rows_and_zero_max_len():
     say("attend empty")
     check_attend("fp8", [0, 0, 0], 8, 2, 128, 16)
