@@ -170,8 +170,13 @@ __global__ __launch_bounds__(256, waves_for(D)) void attn_units_kernel(AttnArgs 
   constexpr int VW = VC * E / 4;               // their 32-bit words
   constexpr int QF = D / 32;                   // products over the channels
   constexpr int OS = D + 4;                    // row stride of the waves' sums in LDS
+  // Where Q's fragments are: in registers, or (256 bf16 channels, whose K, V and
+  // sums leave no room for them) in LDS, a quarter written by each wave
+  constexpr bool QL = D == 256 && E == 2;
+  constexpr int QR = QL ? QF / kWaves : QF;    // fragments that a wave loads
   __shared__ float so[kWaves][16][OS];
   __shared__ float sm[kWaves][16], sl[kWaves][16];
+  __shared__ u32x4 sq[QL ? QF : 1][QL ? 64 : 1];
   __shared__ uint32_t scan[kWaves + 2];
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -220,7 +225,7 @@ __global__ __launch_bounds__(256, waves_for(D)) void attn_units_kernel(AttnArgs 
   int lo, end, t, hk, nh, head0, last;
   bool whole;
   const int* pages;
-  u32x4 qf[QF];
+  u32x4 qf[QR];
   const int tp = a.c.ps >> 4;
   // the page of the 16 tokens from t on (past the end: of the last ones), its
   // number, and the cache row; row 0 stands in where there is nothing to read
@@ -305,8 +310,9 @@ __global__ __launch_bounds__(256, waves_for(D)) void attn_units_kernel(AttnArgs 
     pages = a.pages + (int64_t)b * a.max_pages;
     // Q fragments: head c16, the channels that the K loads bring
 #pragma unroll
-    for (int m = 0; m < QF; ++m) {
-      const int d = E == 2 ? 32 * m + 8 * g : 64 * (m >> 1) + 16 * g + 8 * (m & 1);
+    for (int m = 0; m < QR; ++m) {
+      const int f = QL ? QR * wave + m : m;
+      const int d = E == 2 ? 32 * f + 8 * g : 64 * (f >> 1) + 16 * g + 8 * (f & 1);
       qf[m] = u32x4{0, 0, 0, 0};
       if (c16 < nh) qf[m] = *(const u32x4*)(a.q + b * a.qrow + (int64_t)(head0 + c16) * D + d);
     }
@@ -373,6 +379,11 @@ __global__ __launch_bounds__(256, waves_for(D)) void attn_units_kernel(AttnArgs 
       __syncthreads();                         // the sums in LDS have been read
     }
     if (!more) return;
+    if (QL) {
+#pragma unroll
+      for (int m = 0; m < QR; ++m) sq[QR * wave + m][lane] = qf[m];
+      __syncthreads();
+    }
 #pragma unroll
     for (int j = 0; j < VC; ++j) o[j] = f32x4{0.f, 0.f, 0.f, 0.f};
     m = kLowest;
@@ -383,12 +394,12 @@ __global__ __launch_bounds__(256, waves_for(D)) void attn_units_kernel(AttnArgs 
       id0 = uniform(pages, page_at(t + 2 * kRound));
       id1 = uniform(pages, page_at(t + 2 * kRound + 16));
       // scores of tokens 16 i + 4 g + e for head c16
-      f32x4 s[2];
+      f32x4 s[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        s[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int mm = 0; mm < QF; ++mm) {
+        const u32x4 q = QL ? sq[QL ? mm : 0][QL ? lane : 0] : qf[QL ? 0 : mm];
 #pragma unroll
-        for (int mm = 0; mm < QF; ++mm) {
+        for (int i = 0; i < 2; ++i) {
           u32x4 kk;
           if constexpr (E == 2) {
             kk = kf[i][mm];
@@ -396,8 +407,11 @@ __global__ __launch_bounds__(256, waves_for(D)) void attn_units_kernel(AttnArgs 
             const uint32_t w0 = kf[i][mm >> 1][2 * (mm & 1)], w1 = kf[i][mm >> 1][2 * (mm & 1) + 1];
             kk = u32x4{codes2<FMT, false>(w0), codes2<FMT, true>(w0), codes2<FMT, false>(w1), codes2<FMT, true>(w1)};
           }
-          s[i] = mfma16(kk, qf[mm], s[i]);
+          s[i] = mfma16(kk, q, s[i]);
         }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
         if (E == 1) s[i] *= ks[i] * a.scale2;
         else s[i] *= a.scale2;
       }
