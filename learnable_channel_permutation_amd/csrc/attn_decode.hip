@@ -36,7 +36,6 @@ constexpr float kLowest = -3.402823466e38f;  // running maximum before any token
 constexpr float kLazy = 8.f;                 // the maximum follows once a score passes it by this (in log2)
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a), as_bf16x8(b), c, 0, 0, 0);

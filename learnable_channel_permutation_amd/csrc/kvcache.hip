@@ -133,109 +133,83 @@ __device__ __forceinline__ uint2 encode8(const float* f, float s, float inv) {
   return w;
 }
 
-// Items: (token, group of heads, unit). A unit is 16 channels of a head row:
-// two chunks of 8, a rotary pair's halves or neighbours; the D / 16 units of a
-// row are adjacent lanes, which find its maximum among themselves. A thread
-// handles the same unit of N heads with one read of the table. Groups come as
-// those of q, of k, of v.
-struct AppendItems {
-  int gq, gkv;           // groups of N heads of q, and of k (and of v)
-  int64_t n;
-};
-
-template <int FMT, int D, int N>
-__global__ __launch_bounds__(256) void kv_append_kernel(KvAppendArgs a, AppendItems it) {
+// One thread per (token, head row of q, k or v, unit). A unit is 16 channels of a
+// row, two chunks of 8 chosen as in the rotary kernel; the D / 16 units of a row
+// are adjacent lanes, which find its maximum among themselves, so that K is read,
+// rotated, quantised and written in one pass. The bytes bound it: a row is read
+// once and its codes written once. 16001 tokens x (32 + 32 + 32) heads of 128,
+// fp8 (655 MB), with the read back of 20097 slots (494 MB): one wave a row and one
+// thread an element 1320 us, these two kernels 192 us = 6.1 TB/s.
+template <int FMT, int D, bool STREAM>
+__global__ __launch_bounds__(256) void kv_append_kernel(KvAppendArgs a, int64_t n) {
   typedef RopeChunk<uint16_t, 8> C;
   constexpr int U = D / 16;
   const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (id >= it.n) return;                      // n is a multiple of U: rows leave whole
-  const uint32_t per = (uint32_t)((it.gq + 2 * it.gkv) * U);
+  if (id >= n) return;                         // n is a multiple of U: rows leave whole
+  const uint32_t per = (uint32_t)((a.q.heads + 2 * a.c.heads) * U);
   const int t = (int)(id / per);
   const uint32_t in = (uint32_t)(id - (int64_t)t * per);
   const int u = (int)(in % U);
   int h = (int)(in / U);
-  const int which = h < it.gq ? 0 : h < it.gq + it.gkv ? 1 : 2;    // q, k, v
-  h -= which == 0 ? 0 : which == 1 ? it.gq : it.gq + it.gkv;
-  const Rows r = which == 0 ? a.q : which == 1 ? a.k : a.v;
-  const int step = which == 0 ? it.gq : it.gkv;
-  const bool turn = which != 2 && 16 * u < a.rot, split = turn && !a.interleaved;
-  const int d0 = split ? 8 * u : 16 * u, d1 = split ? d0 + a.rot / 2 : d0 + 8;
-  const uint16_t* x = (const uint16_t*)r.x + t * r.xt;
-  u32x4 w0[N], w1[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-    if (h + i * step < r.heads) {
-      const uint16_t* xi = x + (h + i * step) * r.xh;
-      w0[i] = *(const u32x4*)(xi + d0);
-      w1[i] = *(const u32x4*)(xi + d1);
-    }
-  float c[8], s[8];
+  const int which = h < a.q.heads ? 0 : h < a.q.heads + a.c.heads ? 1 : 2;   // q, k, v
+  h -= which == 0 ? 0 : which == 1 ? a.q.heads : a.q.heads + a.c.heads;
+  const Rows& r = which == 0 ? a.q : which == 1 ? a.k : a.v;
+  // V, and rows that are not rotated, have no pairs and split at D / 2
+  const int rot = which == 2 ? 0 : a.rot;
+  const bool turn = 16 * u < rot;
+  const int d0 = turn ? 8 * u : rot + 8 * (u - rot / 16), d1 = d0 + (turn ? rot : D - rot) / 2;
+  const uint16_t* x = (const uint16_t*)r.x + t * r.xt + h * r.xh;
+  const u32x4 w0 = load_as<STREAM, u32x4>(x + d0), w1 = load_as<STREAM, u32x4>(x + d1);
+  float f[16];
+  C::unpack(w0, f);
+  C::unpack(w1, f + 8);
   if (turn) {
     const int p = min(max(a.pos[t], 0), a.max_pos - 1);
-    const floatx4* tab = (const floatx4*)(a.table + (int64_t)p * (a.rot / 2) + 8 * u);
+    const float2* tab = a.table + (int64_t)p * (rot / 2) + (a.interleaved ? d0 / 2 : d0);
+    const int skip = a.interleaved ? (rot / 2 - 8) / 2 : 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const floatx4 q = tab[j];
-      c[2 * j] = q[0]; c[2 * j + 1] = q[2];
-      s[2 * j] = q[1]; s[2 * j + 1] = q[3];
-    }
-  }
-  int64_t row = -1;
-  if (which != 0) {
-    const int slot = a.slots[t];
-    if (slot >= 0 && slot < a.c.pages * a.c.ps) {
-      const int page = slot / a.c.ps;
-      row = (int64_t)page * a.c.heads * a.c.ps + (slot - page * a.c.ps);
-    }
-  }
+    for (int j = 0; j < 8; j += 2) {
+      const floatx4 cs = *(const floatx4*)(tab + j + (j >= 4 ? skip : 0));
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    if (h + i * step >= r.heads) break;
-    float f[16];
-    C::unpack(w0[i], f);
-    C::unpack(w1[i], f + 8);
-    if (turn) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        float& y0 = f[a.interleaved ? 2 * j : j];
-        float& y1 = f[a.interleaved ? 2 * j + 1 : j + 8];
-        const float p = y0, q = y1;
-        y0 = rot_first(p, q, c[j], s[j]);
-        y1 = rot_second(p, q, c[j], s[j]);
+      for (int i = 0; i < 2; ++i) {
+        float& y0 = f[a.interleaved ? 2 * (j + i) : j + i];
+        float& y1 = f[a.interleaved ? 2 * (j + i) + 1 : j + i + 8];
+        const float p0 = y0, p1 = y1;
+        y0 = rot_first(p0, p1, cs[2 * i], cs[2 * i + 1]);
+        y1 = rot_second(p0, p1, cs[2 * i], cs[2 * i + 1]);
       }
     }
-    if (which == 0) {
-      uint16_t* y = (uint16_t*)r.y + t * r.yt + (h + i * step) * r.yh;
-      *(u32x4*)(y + d0) = C::pack(f);
-      *(u32x4*)(y + d1) = C::pack(f + 8);
-      continue;
-    }
-    const int64_t at = row + (int64_t)(h + i * step) * a.c.ps;
-    char* dst = (char*)(which == 1 ? a.c.k : a.c.v);
-    if (FMT == KV_BF16) {
-      if (row >= 0) {
-        *(u32x4*)(dst + (at * D + d0) * 2) = C::pack(f);
-        *(u32x4*)(dst + (at * D + d1) * 2) = C::pack(f + 8);
-      }
-      continue;
-    }
-    uint32_t top = 0;
-#pragma unroll
-    for (int j = 0; j < 16; ++j) top = max(top, __float_as_uint(f[j]) & 0x7fffffffu);
-    top = row_top<U>(top);
-    const float sc = row_scale(top, FMT), inv = 1.f / sc;
-    uint2 c0 = encode8<FMT>(f, sc, inv), c1 = encode8<FMT>(f + 8, sc, inv);
-    if (top >= 0x7f800000u) c0 = c1 = make_uint2(0u, 0u);
-    if (row >= 0) {
-      *(uint2*)(dst + at * D + d0) = c0;
-      *(uint2*)(dst + at * D + d1) = c1;
-      if (u == 0) (which == 1 ? a.c.ks : a.c.vs)[at] = sc;
-    }
   }
+  if (which == 0) {
+    uint16_t* y = (uint16_t*)r.y + t * r.yt + h * r.yh;
+    store_as<STREAM, u32x4>(y + d0, C::pack(f));
+    store_as<STREAM, u32x4>(y + d1, C::pack(f + 8));
+    return;
+  }
+  const int slot = a.slots[t];
+  if (slot < 0 || slot >= a.c.pages * a.c.ps) return;          // a row's lanes together
+  const int page = slot / a.c.ps;
+  const int64_t row = ((int64_t)page * a.c.heads + h) * a.c.ps + (slot - page * a.c.ps);
+  char* dst = (char*)(which == 1 ? a.c.k : a.c.v);
+  if (FMT == KV_BF16) {
+    *(u32x4*)(dst + (row * D + d0) * 2) = C::pack(f);
+    *(u32x4*)(dst + (row * D + d1) * 2) = C::pack(f + 8);
+    return;
+  }
+  uint32_t top = 0;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) top = max(top, __float_as_uint(f[j]) & 0x7fffffffu);
+  top = row_top<U>(top);
+  const float sc = row_scale(top, FMT), inv = 1.f / sc;
+  uint2 c0 = encode8<FMT>(f, sc, inv), c1 = encode8<FMT>(f + 8, sc, inv);
+  if (top >= 0x7f800000u) c0 = c1 = make_uint2(0u, 0u);
+  *(uint2*)(dst + row * D + d0) = c0;          // the halves of a line come by different stores: not streamed
+  *(uint2*)(dst + row * D + d1) = c1;
+  if (u == 0) (which == 1 ? a.c.ks : a.c.vs)[row] = sc;
 }
 
 // One thread per eight channels of a slot and head, K and V.
-template <int FMT, bool BF>
+template <int FMT, bool BF, bool STREAM>
 __global__ __launch_bounds__(256) void kv_read_kernel(KvCache c, const int* slots, int64_t n, char* ko, char* vo) {
   const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (id >= n) return;
@@ -251,19 +225,19 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvCache c, const int* slot
     for (int i = 0; i < 2; ++i) {
       const char* src = (const char*)(i ? c.v : c.k);
       if (FMT == KV_BF16) {
-        RopeChunk<uint16_t, 8>::unpack(*(const u32x4*)(src + (row * c.D + d) * 2), f[i]);
+        RopeChunk<uint16_t, 8>::unpack(load_as<STREAM, u32x4>(src + (row * c.D + d) * 2), f[i]);
       } else {
-        const uint2 w = *(const uint2*)(src + row * c.D + d);
+        const u32x2 w = load_as<STREAM, u32x2>(src + row * c.D + d);
         const float s = (i ? c.vs : c.ks)[row];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const int word = (int)(j < 4 ? w.x : w.y);
+          const int word = (int)w[j >> 2];
           if (FMT == KV_INT8) f[i][j] = (float)(int8_t)(word >> (8 * (j & 3)));
         }
         if (FMT == KV_E4M3) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const int word = (int)(j ? w.y : w.x);
+            const int word = (int)w[j];
             const auto a = __builtin_amdgcn_cvt_pk_f32_fp8(word, false), b = __builtin_amdgcn_cvt_pk_f32_fp8(word, true);
             f[i][4 * j] = a[0]; f[i][4 * j + 1] = a[1]; f[i][4 * j + 2] = b[0]; f[i][4 * j + 3] = b[1];
           }
@@ -277,46 +251,44 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvCache c, const int* slot
   for (int i = 0; i < 2; ++i) {
     char* dst = i ? vo : ko;
     if (BF) {
-      *(u32x4*)(dst + id * 16) = RopeChunk<uint16_t, 8>::pack(f[i]);
+      store_as<STREAM, u32x4>(dst + id * 16, RopeChunk<uint16_t, 8>::pack(f[i]));
     } else {
-      *(floatx4*)(dst + id * 32) = floatx4{f[i][0], f[i][1], f[i][2], f[i][3]};
-      *(floatx4*)(dst + id * 32 + 16) = floatx4{f[i][4], f[i][5], f[i][6], f[i][7]};
+      store_as<STREAM, floatx4>(dst + id * 32, floatx4{f[i][0], f[i][1], f[i][2], f[i][3]});
+      store_as<STREAM, floatx4>(dst + id * 32 + 16, floatx4{f[i][4], f[i][5], f[i][6], f[i][7]});
     }
   }
 }
 
-template <int FMT, int D, int N>
-hipError_t run_append(const KvAppendArgs& a, hipStream_t s) {
-  AppendItems it{};
-  it.gq = (a.q.heads + N - 1) / N;
-  it.gkv = (a.c.heads + N - 1) / N;
-  it.n = (int64_t)a.T * (it.gq + 2 * it.gkv) * (D / 16);
-  const int64_t grid = (it.n + 255) / 256;
-  if (grid > 0x7fffffff) return hipErrorInvalidValue;
-  kv_append_kernel<FMT, D, N><<<(unsigned)grid, 256, 0, s>>>(a, it);
-  return hipGetLastError();
-}
-
 template <int FMT, int D>
-hipError_t run_append_n(const KvAppendArgs& a, hipStream_t s) {
-  const int64_t items = (int64_t)a.T * (a.q.heads + 2 * a.c.heads) * (D / 16);
-  return items >= (int64_t)4 * 256 * 1024 ? run_append<FMT, D, 4>(a, s) : run_append<FMT, D, 1>(a, s);
+hipError_t run_append(const KvAppendArgs& a, hipStream_t s) {
+  const int64_t rows = (int64_t)a.T * (a.q.heads + 2 * a.c.heads), n = rows * (D / 16), grid = (n + 255) / 256;
+  if (grid > 0x7fffffff) return hipErrorInvalidValue;
+  const int64_t q = (int64_t)a.T * a.q.heads * D * 4, kv = (int64_t)a.T * a.c.heads * 2 * D * (FMT == KV_BF16 ? 4 : 3);
+  if (q + kv > kStreamBytes) kv_append_kernel<FMT, D, true><<<(unsigned)grid, 256, 0, s>>>(a, n);
+  else kv_append_kernel<FMT, D, false><<<(unsigned)grid, 256, 0, s>>>(a, n);
+  return hipGetLastError();
 }
 
 template <int FMT>
 hipError_t run_append_d(const KvAppendArgs& a, hipStream_t s) {
-  if (a.c.D == 64) return run_append_n<FMT, 64>(a, s);
-  if (a.c.D == 128) return run_append_n<FMT, 128>(a, s);
-  return run_append_n<FMT, 256>(a, s);
+  if (a.c.D == 64) return run_append<FMT, 64>(a, s);
+  if (a.c.D == 128) return run_append<FMT, 128>(a, s);
+  return run_append<FMT, 256>(a, s);
+}
+
+template <int FMT, bool BF>
+hipError_t run_read(const KvCache& c, const int* slots, int T, void* k, void* v, hipStream_t s) {
+  const int64_t n = (int64_t)T * c.heads * (c.D / 8), grid = (n + 255) / 256;
+  if (grid > 0x7fffffff) return hipErrorInvalidValue;
+  const bool stream = n * 16 * ((FMT == KV_BF16 ? 2 : 1) + (BF ? 2 : 4)) > kStreamBytes;
+  if (stream) kv_read_kernel<FMT, BF, true><<<(unsigned)grid, 256, 0, s>>>(c, slots, n, (char*)k, (char*)v);
+  else kv_read_kernel<FMT, BF, false><<<(unsigned)grid, 256, 0, s>>>(c, slots, n, (char*)k, (char*)v);
+  return hipGetLastError();
 }
 
 template <int FMT>
-hipError_t run_read(const KvCache& c, const int* slots, int T, void* k, void* v, int bf16, hipStream_t s) {
-  const int64_t n = (int64_t)T * c.heads * (c.D / 8), grid = (n + 255) / 256;
-  if (grid > 0x7fffffff) return hipErrorInvalidValue;
-  if (bf16) kv_read_kernel<FMT, true><<<(unsigned)grid, 256, 0, s>>>(c, slots, n, (char*)k, (char*)v);
-  else kv_read_kernel<FMT, false><<<(unsigned)grid, 256, 0, s>>>(c, slots, n, (char*)k, (char*)v);
-  return hipGetLastError();
+hipError_t run_read_bf(const KvCache& c, const int* slots, int T, void* k, void* v, int bf16, hipStream_t s) {
+  return bf16 ? run_read<FMT, true>(c, slots, T, k, v, s) : run_read<FMT, false>(c, slots, T, k, v, s);
 }
 
 }  // namespace
@@ -336,9 +308,9 @@ hipError_t launch_kv_append(const KvAppendArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_kv_read(const KvCache& c, const int* slots, int T, void* k, void* v, int bf16, hipStream_t s) {
-  if (c.format == KV_BF16) return run_read<KV_BF16>(c, slots, T, k, v, bf16, s);
-  if (c.format == KV_E4M3) return run_read<KV_E4M3>(c, slots, T, k, v, bf16, s);
-  return run_read<KV_INT8>(c, slots, T, k, v, bf16, s);
+  if (c.format == KV_BF16) return run_read_bf<KV_BF16>(c, slots, T, k, v, bf16, s);
+  if (c.format == KV_E4M3) return run_read_bf<KV_E4M3>(c, slots, T, k, v, bf16, s);
+  return run_read_bf<KV_INT8>(c, slots, T, k, v, bf16, s);
 }
 
 }  // namespace lcp

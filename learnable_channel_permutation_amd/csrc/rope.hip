@@ -64,92 +64,72 @@ __global__ void rope_pairs_kernel(RopeArgs a, int64_t n) {
   store(out, y + d1, v * cs.x + u * s);
 }
 
-// Items of the vector kernel: (token, group of heads, unit). A unit is 2 V
-// channels of a head row, V pairs: the chunks [V u, +V) and [V u + rot / 2, +V)
-// (half layout) or two adjacent chunks (interleaved and unrotated channels).
-// A thread keeps its pairs' cosines and sines and applies them to the same
-// unit of N heads, whose loads it issues together. It reads both chunks of a
-// pair before it writes them, so in place needs nothing more.
-// The bytes of the rows bound it. At 16384 tokens x 80 heads of 128 bf16
-// (680 MB): one thread a pair 452 us (1.5 TB/s), see launch_rope for this one.
-struct RopeItems {
-  int gq, gk;            // groups of N heads of q and of k
-  int units, rotated;    // units of a row, and those that are rotated
-  int64_t n;             // items
-};
-
-template <typename E, int V, int N>
-__global__ __launch_bounds__(256) void rope_units_kernel(RopeArgs a, RopeItems it) {
+// One thread per (token, head, unit). A unit is 2 V channels of a head row, V
+// pairs: the chunks [V u, +V) and [V u + rot / 2, +V), in the half layout a
+// pair's two channels; the unrotated channels are split alike. Adjacent lanes
+// take adjacent chunks, so that every load and store of a wave covers whole
+// lines (two adjacent chunks a lane measured 4 % slower, and 30 % with streaming
+// stores). A thread reads both chunks before it writes them: in place needs
+// nothing more. The bytes of the rows bound it; the table's rows, which all
+// heads of a token share, come from the caches (a thread that kept its table
+// entries for 2 or 4 heads was 0 - 8 % slower: fewer loads in flight).
+// 16384 tokens x 80 heads of 128 bf16 (680 MB): one thread a pair 452 us, this
+// 110 us = 6.2 TB/s; 8191 x 72, 306 MB: 184 -> 51 us = 6.0 TB/s.
+template <typename E, int V, bool STREAM>
+__global__ __launch_bounds__(256) void rope_units_kernel(RopeArgs a, int64_t n) {
   typedef RopeChunk<E, V> C;
+  typedef typename C::T W;
   const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (id >= it.n) return;
-  const uint32_t per = (uint32_t)((it.gq + it.gk) * it.units);
+  if (id >= n) return;
+  const int units = a.D / (2 * V), rotated = a.rot / (2 * V);
+  const uint32_t per = (uint32_t)((a.q.heads + a.k.heads) * units);
   const int t = (int)(id / per);
   const uint32_t in = (uint32_t)(id - (int64_t)t * per);
-  const int u = (int)(in % it.units);
-  int h = (int)(in / it.units);
-  const bool isk = h >= it.gq;
-  if (isk) h -= it.gq;
-  const Rows r = isk ? a.k : a.q;
-  const int step = isk ? it.gk : it.gq;        // heads h, h + step, .. : neighbours in a wave are neighbours in memory
-  const bool turn = u < it.rotated, split = turn && !a.interleaved;
-  const int d0 = split ? V * u : 2 * V * u, d1 = split ? d0 + a.rot / 2 : d0 + V;
-  const E* x = (const E*)r.x + t * r.xt;
-  E* y = (E*)r.y + t * r.yt;
-  typename C::T w0[N], w1[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-    if (h + i * step < r.heads) {
-      const E* xi = x + (h + i * step) * r.xh;
-      w0[i] = *(const typename C::T*)(xi + d0);
-      w1[i] = *(const typename C::T*)(xi + d1);
-    }
-  float c[V], s[V];
+  const int u = (int)(in % units);
+  int h = (int)(in / units);
+  const bool isk = h >= a.q.heads;
+  if (isk) h -= a.q.heads;
+  const Rows& r = isk ? a.k : a.q;
+  const bool turn = u < rotated;
+  const int d0 = turn ? V * u : a.rot + V * (u - rotated), d1 = d0 + (turn ? a.rot : a.D - a.rot) / 2;
+  const E* x = (const E*)r.x + t * r.xt + h * r.xh;
+  E* y = (E*)r.y + t * r.yt + h * r.yh;
+  W w0 = load_as<STREAM, W>(x + d0), w1 = load_as<STREAM, W>(x + d1);
   if (turn) {
     const int p = min(max(a.pos[t], 0), a.max_pos - 1);
-    const floatx4* tab = (const floatx4*)(a.table + (int64_t)p * (a.rot / 2) + V * u);
+    // V pairs from d0 on, or half of them from each chunk
+    const float2* tab = a.table + (int64_t)p * (a.rot / 2) + (a.interleaved ? d0 / 2 : d0);
+    const int skip = a.interleaved ? (a.rot / 2 - V) / 2 : 0;
+    float f[2 * V];
+    C::unpack(w0, f);
+    C::unpack(w1, f + V);
 #pragma unroll
-    for (int j = 0; j < V / 2; ++j) {
-      const floatx4 q = tab[j];
-      c[2 * j] = q[0]; c[2 * j + 1] = q[2];
-      s[2 * j] = a.inverse ? -q[1] : q[1]; s[2 * j + 1] = a.inverse ? -q[3] : q[3];
-    }
-  }
+    for (int j = 0; j < V; j += 2) {
+      const floatx4 cs = *(const floatx4*)(tab + j + (j >= V / 2 ? skip : 0));
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    if (h + i * step >= r.heads) break;
-    if (turn) {
-      float f[2 * V];
-      C::unpack(w0[i], f);
-      C::unpack(w1[i], f + V);
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        float& u0 = f[a.interleaved ? 2 * j : j];
-        float& u1 = f[a.interleaved ? 2 * j + 1 : j + V];
-        const float p = u0, q = u1;
-        u0 = p * c[j] - q * s[j];
-        u1 = q * c[j] + p * s[j];
+      for (int i = 0; i < 2; ++i) {
+        float& u0 = f[a.interleaved ? 2 * (j + i) : j + i];
+        float& u1 = f[a.interleaved ? 2 * (j + i) + 1 : j + i + V];
+        const float c = cs[2 * i], s = a.inverse ? -cs[2 * i + 1] : cs[2 * i + 1], p0 = u0, p1 = u1;
+        u0 = p0 * c - p1 * s;
+        u1 = p1 * c + p0 * s;
       }
-      w0[i] = C::pack(f);
-      w1[i] = C::pack(f + V);
     }
-    E* yi = y + (h + i * step) * r.yh;
-    *(typename C::T*)(yi + d0) = w0[i];
-    *(typename C::T*)(yi + d1) = w1[i];
+    w0 = C::pack(f);
+    w1 = C::pack(f + V);
   }
+  store_as<STREAM, W>(y + d0, w0);
+  store_as<STREAM, W>(y + d1, w1);
 }
 
-template <typename E, int V, int N>
+template <typename E, int V>
 hipError_t run_units(const RopeArgs& a, hipStream_t s) {
-  RopeItems it{};
-  it.gq = (a.q.heads + N - 1) / N;
-  it.gk = (a.k.heads + N - 1) / N;
-  it.units = a.D / (2 * V);
-  it.rotated = a.rot / (2 * V);
-  it.n = (int64_t)a.T * (it.gq + it.gk) * it.units;
-  const int64_t grid = (it.n + 255) / 256;
+  const int64_t rows = (int64_t)a.T * (a.q.heads + a.k.heads), n = rows * (a.D / (2 * V)), grid = (n + 255) / 256;
   if (grid > 0x7fffffff) return hipErrorInvalidValue;
-  rope_units_kernel<E, V, N><<<(unsigned)grid, 256, 0, s>>>(a, it);
+  if (rows * a.D * 2 * (int64_t)sizeof(E) > kStreamBytes)
+    rope_units_kernel<E, V, true><<<(unsigned)grid, 256, 0, s>>>(a, n);
+  else
+    rope_units_kernel<E, V, false><<<(unsigned)grid, 256, 0, s>>>(a, n);
   return hipGetLastError();
 }
 
@@ -168,22 +148,13 @@ hipError_t launch_rope_table(const RopeFreq& f, int max_pos, float2* table, hipS
   return hipGetLastError();
 }
 
-// Heads of a thread: 4 share one read of the table once that still leaves
-// every CU work for several waves, else 1 (a decode step's rows are spread as
-// wide as they go).
-template <typename E, int V>
-hipError_t run_vector(const RopeArgs& a, hipStream_t s) {
-  const int64_t items = (int64_t)a.T * (a.q.heads + a.k.heads) * (a.D / (2 * V));
-  return items >= (int64_t)4 * 256 * 1024 ? run_units<E, V, 4>(a, s) : run_units<E, V, 1>(a, s);
-}
-
 hipError_t launch_rope(const RopeArgs& a, int bf16, hipStream_t s) {
   const auto fits = [&](int V, int e) {
     return a.D % (2 * V) == 0 && a.rot % (2 * V) == 0 && chunked(a.q, V, e) && chunked(a.k, V, e);
   };
-  if (bf16 && fits(8, 2)) return run_vector<uint16_t, 8>(a, s);
-  if (bf16 && fits(4, 2)) return run_vector<uint16_t, 4>(a, s);
-  if (!bf16 && fits(4, 4)) return run_vector<float, 4>(a, s);
+  if (bf16 && fits(8, 2)) return run_units<uint16_t, 8>(a, s);
+  if (bf16 && fits(4, 2)) return run_units<uint16_t, 4>(a, s);
+  if (!bf16 && fits(4, 4)) return run_units<float, 4>(a, s);
   const int64_t n = (int64_t)a.T * (a.q.heads + a.k.heads) * (a.rot / 2 + a.D - a.rot);
   const int64_t grid = (n + 255) / 256;
   if (grid > 0x7fffffff) return hipErrorInvalidValue;
