@@ -74,7 +74,7 @@ __global__ void rope_pairs_kernel(RopeArgs a, int64_t n) {
 // heads of a token share, come from the caches (a thread that kept its table
 // entries for 2 or 4 heads was 0 - 8 % slower: fewer loads in flight).
 // 16384 tokens x 80 heads of 128 bf16 (680 MB): one thread a pair 452 us, this
-// 110 us = 6.2 TB/s; 8191 x 72, 306 MB: 184 -> 51 us = 6.0 TB/s.
+// 114 us = 6.0 TB/s; 8191 x 72, 306 MB: 184 -> 54 us = 5.7 TB/s.
 template <typename E, int V, bool STREAM>
 __global__ __launch_bounds__(256) void rope_units_kernel(RopeArgs a, int64_t n) {
   typedef RopeChunk<E, V> C;

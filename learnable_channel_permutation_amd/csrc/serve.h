@@ -48,11 +48,11 @@ struct RopeChunk<float, 4> {
 
 // Loads and stores of data that nobody finds in the caches again: a call that
 // moves more than the 256 MB of the last-level cache hints them as streaming.
-// Measured on the rotary kernel, 72 heads of 128 bf16, plain against hinted
-// (us): 75 MB 14.4 / 16.1, 302 MB 50.7 / 51.8, 453 MB 80.7 / 75.3, 604 MB
-// 105.8 / 99.7; writing 16001 tokens into the cache and reading 20097 back
-// (655 + 494 MB) 228 / 192.
-constexpr int64_t kStreamBytes = (int64_t)384 << 20;
+// Measured on the rotary kernel (72 heads of 128 bf16) with a kernel that reads
+// its result, plain against hinted (us): 77 MB 27.4 / 29.5, 153 MB 51.1 / 51.9,
+// 306 MB 107.5 / 100.2, 612 MB 199.3 / 192.3; writing 16001 tokens into the
+// cache and reading 20097 back (655 + 494 MB) 237 / 208.
+constexpr int64_t kStreamBytes = (int64_t)256 << 20;
 template <bool STREAM, typename T>
 __device__ __forceinline__ T load_as(const void* p) {
   if (STREAM) return __builtin_nontemporal_load((const T*)p);
