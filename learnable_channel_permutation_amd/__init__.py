@@ -16,7 +16,8 @@ from ._lib import (LCP_BF16, LCP_F32, LcpError, lcp_colnorm, lcp_error,  # noqa:
                    lcp_step_workspace_bytes, lcp_xt_pitch, make_cfg, make_layer, make_timing,
                    lcp_adamw, lcp_step_bwd_adamw, lcp_train, make_adamw_cfg, lcp_layer_outputs,
                    lcp_attn_decode, lcp_attn_decode_workspace_bytes, lcp_kv_append, lcp_kv_read, lcp_rope,
-                   lcp_rope_table, make_kv_cache, make_rope_cfg)
+                   lcp_rope_table, make_kv_cache, make_rope_cfg, lcp_deploy_forward, lcp_gather_channels,
+                   lcp_layer_outputs_noalloc, lcp_sparse_gemm, lcp_sparse_pack, lcp_sparse_pack_bytes)
 
 __all__ = ["LayerSession", "LcpError", "PagedKVCache"] + [n for n in _lib.EXPORTS if n.startswith("lcp_")]
 
@@ -156,9 +157,9 @@ class PagedKVCache:
         """The stored k and v of slots, [T, heads, D] bfloat16 unless outputs are given (lcp_kv_read)."""
         shape = (slots.shape[0], self.c.heads, self.c.D)
         if k_out is None:
-            k_out = _used_on(stream, torch.empty(shape, dtype=torch.bfloat16, device=slots.device))
+            k_out = _used_on(stream, slots.new_empty(shape, dtype=torch.bfloat16))
         if v_out is None:
-            v_out = _used_on(stream, torch.empty(shape, dtype=k_out.dtype, device=slots.device))
+            v_out = _used_on(stream, torch.empty_like(k_out))
         lcp_kv_read(self.c, slots, k_out, v_out, stream)
         return k_out, v_out
 

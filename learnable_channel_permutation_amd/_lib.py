@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -131,9 +132,9 @@ def _load():
         "lcp_sparse_gemm": (i, [vp, vp, vp, i, i, i, vp, vp]),
         "lcp_deploy_forward": (i, [vp, vp, vp, i, vp, i, i, i, vp, vp, vp]),
         "lcp_rope_table": (i, [ctypes.POINTER(lcp_rope_cfg), i, vp, vp]),
-        "lcp_rope": (i, [ctypes.POINTER(lcp_heads), ctypes.POINTER(lcp_heads), i, i, i, vp, i, vp, i, i, i, vp]),
-        "lcp_kv_append": (i, [ctypes.POINTER(lcp_kv_cache), ctypes.POINTER(lcp_heads), ctypes.POINTER(lcp_heads),
-                              ctypes.POINTER(lcp_heads), i, vp, vp, i, vp, i, i, vp]),
+        # head rows (vp): an lcp_heads by reference, or its bytes
+        "lcp_rope": (i, [vp, vp, i, i, i, vp, i, vp, i, i, i, vp]),
+        "lcp_kv_append": (i, [ctypes.POINTER(lcp_kv_cache), vp, vp, vp, i, vp, vp, i, vp, i, i, vp]),
         "lcp_kv_read": (i, [ctypes.POINTER(lcp_kv_cache), vp, i, vp, vp, i, vp]),
         "lcp_attn_decode_workspace_bytes": (i, [ctypes.POINTER(lcp_kv_cache), i, i, i, i, psz]),
         "lcp_attn_decode": (i, [ctypes.POINTER(lcp_kv_cache), vp, ctypes.c_int64, i, i, vp, i, vp, i, f, i, vp, i, vp,
@@ -372,20 +373,27 @@ def _index(t, n, name):
     return t.data_ptr()
 
 
+# the layout of lcp_heads; packing it takes a quarter of the time of filling the ctypes structure
+_pack_heads = struct.Struct("PPi4xqqqq").pack
+
+
 def _heads(x, y, D, dtype, name):
-    """Head rows [T, heads, D] (any strides, channels contiguous)."""
+    """Head rows [T, heads, D] (any strides, channels contiguous) as the bytes of an lcp_heads."""
     shape = x.shape
     if len(shape) != 3 or shape[2] != D or x.dtype is not dtype:
         raise ValueError("%s must be [T, heads, %d] %s" % (name, D, dtype))
-    st, sh, sd = x.stride()
-    if sd != 1:
-        raise ValueError("%s must have contiguous channels" % name)
+    st, sh, one = x.stride()
+    yone = 1
     if y is None:
-        return lcp_heads(x.data_ptr(), None, shape[1], st, sh, 0, 0)
-    if y.shape != shape or y.dtype is not dtype or y.stride(2) != 1:
-        raise ValueError("the output of %s must have its shape and dtype and contiguous channels" % name)
-    yt, yh, _ = y.stride()
-    return lcp_heads(x.data_ptr(), y.data_ptr(), shape[1], st, sh, yt, yh)
+        yp = yt = yh = 0
+    else:
+        if y.shape != shape or y.dtype is not dtype:
+            raise ValueError("the output of %s must have its shape and dtype" % name)
+        yp = y.data_ptr()
+        yt, yh, yone = y.stride()
+    if one != 1 or yone != 1:
+        raise ValueError("the channels of %s must be contiguous" % name)
+    return _pack_heads(x.data_ptr(), yp, shape[1], st, sh, yt, yh)
 
 
 def _table(table):
@@ -418,9 +426,9 @@ def lcp_rope(q, q_out, table, pos, k=None, k_out=None, interleaved=False, invers
     if k is not None:
         if k.shape[0] != T or k_out is None:
             raise ValueError("k needs q's number of tokens and an output")
-        hk = ctypes.byref(_heads(k, k_out, D, dtype, "k"))
+        hk = _heads(k, k_out, D, dtype, "k")
     p, max_pos, rot = _table(table)
-    code = LIB.lcp_rope(ctypes.byref(hq), hk, dtype_code(q), T, D, p, max_pos, _index(pos, T, "pos"), rot,
+    code = LIB.lcp_rope(hq, hk, dtype_code(q), T, D, p, max_pos, _index(pos, T, "pos"), rot,
                         1 if interleaved else 0, 1 if inverse else 0, _stream(stream))
     return _check("lcp_rope", code)
 
@@ -455,13 +463,13 @@ def lcp_kv_append(cache, k, v, slots, q=None, q_out=None, table=None, pos=None, 
     if q is not None:
         if q.shape[0] != T or q_out is None or table is None:
             raise ValueError("q needs k's number of tokens, an output and a table")
-        hq = ctypes.byref(_heads(q, q_out, D, _BF16, "q"))
+        hq = _heads(q, q_out, D, _BF16, "q")
     p = pp = None
     max_pos = rot = 0
     if table is not None:
         p, max_pos, rot = _table(table)
         pp = _index(pos, T, "pos")
-    code = LIB.lcp_kv_append(ctypes.byref(cache), hq, ctypes.byref(hk), ctypes.byref(hv), T, _index(slots, T, "slots"),
+    code = LIB.lcp_kv_append(ctypes.byref(cache), hq, hk, hv, T, _index(slots, T, "slots"),
                              p, max_pos, pp, rot, 1 if interleaved else 0, _stream(stream))
     return _check("lcp_kv_append", code)
 

@@ -496,3 +496,20 @@ def test_step_on_another_stream_and_in_a_graph():
         assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])
         assert torch.equal(c.k.view(torch.uint8), want[i][2])
         c.attend(qo, dp, dl, max_len=64)                # eager work in between
+
+
+def test_example_decodes_through_the_deployed_layers():
+    """The attention block of examples/: deployed 2:4 projections, rotary cache write, attention over shared pages."""
+    import importlib.util
+    import os
+    say("example block")
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "sparse_attention_block.py")
+    spec = importlib.util.spec_from_file_location("sparse_attention_block", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    for prompt in (200, 256):
+        err, y = mod.main(["--hidden", "512", "--heads", "8", "--kv-heads", "2", "--prompt", str(prompt), "--steps", "5",
+                           "--batch", "3", "--train-steps", "2"])
+        # bfloat16 output (2^-8) against fp32 on the same bfloat16 reads of fp8 codes, which are exact
+        assert err < 2.0 ** -8 and torch.isfinite(y.float()).all() and y.shape == (3, 512)
