@@ -52,8 +52,8 @@ __device__ __forceinline__ uint32_t codes2(uint32_t w) {
 
 // How the work is dealt. A unit is one sequence, one key/value head and up to 16
 // of its query heads; its work is counted in steps.
-//   direct (wgs == 0): a workgroup a unit, no second kernel. Where no sequence
-//     can have more than kDirect steps.
+//   direct (wgs == 0): a workgroup a unit, no second kernel. Where no unit can
+//     have more than kDirect bytes of K.
 //   else: the steps of all units in a row, each unit led by kExtra steps that
 //     stand for what beginning and ending it costs, cut into parts that differ
 //     by one step at most, whatever the sequences' lengths are. A workgroup finds
@@ -70,8 +70,11 @@ struct Plan {
   float* part;           // [2 wgs][nh][D]
   float2* ml;            // [2 wgs][nh] maximum and sum
 };
-constexpr int kDirect = 16;
-constexpr uint32_t kLeast = 16;     // steps of a part, where there are fewer than wgs such parts
+// Direct against dealt with its second kernel, us a pass: K of 128 KB (1 x 1000
+// fp8) 12.7 / 17.0, 192 KB (1 x 1500; 64 x 1500) 13.8 / 16.9; 27.9 / 31.6,
+// 256 KB (1 x 2000; 8 x 1000 bf16) 18.1 / 17.0; 17.4 / 16.8.
+constexpr int kDirect = 192 << 10;
+constexpr uint32_t kLeast = 12;     // steps of a part, where there are fewer than wgs such parts
 constexpr int kExtra = 8;
 
 // The cut of `all` steps.
@@ -105,13 +108,16 @@ __device__ __forceinline__ void put(void* p, int64_t i, T v) {
   typedef T __attribute__((address_space(1))) * GlobalPtr;
   ((GlobalPtr)(uintptr_t)p)[i] = v;
 }
-__device__ __forceinline__ void put_out(const AttnArgs& a, int64_t i, float v) {
-  if (a.out_bf16) put<uint16_t>(a.out, i, (uint16_t)f2bf(v));
-  else put<float>(a.out, i, v);
-}
-// The log-sum-exp of a row from its maximum and sum in base 2.
-__device__ __forceinline__ void put_lse(const AttnArgs& a, int64_t row, float m, float l) {
-  if (a.lse) put<float>(a.lse, row, l == 0.f ? -__builtin_inff() : (m + log2_(l)) * 0.6931471805599453f);
+// Channels 4 td .. of a finished row from its unscaled sums, and (td 0) its
+// log-sum-exp, from its maximum and sum in base 2.
+template <int D>
+__device__ __forceinline__ void put_row(const AttnArgs& a, int64_t row, int td, f32x4 y, float m, float l) {
+  if (l == 0.f) y = f32x4{0.f, 0.f, 0.f, 0.f};
+  else y /= l;
+  const int64_t i = row * (D / 4) + td;
+  if (a.out_bf16) put<u32x2>(a.out, i, u32x2{pack2(y[0], y[1]), pack2(y[2], y[3])});
+  else put<f32x4>(a.out, i, y);
+  if (td == 0 && a.lse) put<float>(a.lse, row, l == 0.f ? -__builtin_inff() : (m + log2_(l)) * 0.6931471805599453f);
 }
 
 // Tokens of a sequence: the first counted one, the end, and the steps between.
@@ -167,6 +173,8 @@ __global__ __launch_bounds__(256, waves_for(D)) void attn_units_kernel(AttnArgs 
   constexpr int KL = D * E / 64;               // 16-byte K loads of a lane for 16 tokens
   constexpr int VC = D / 16;                   // channels of V a lane holds of each of its 8 tokens
   constexpr int VW = VC * E / 4;               // their 32-bit words
+  constexpr int VP = VC * E > 16 ? 16 / E : VC;        // those that are adjacent: 16 bytes at most, so that the 16
+                                               // lanes of a token cover whole lines with every load
   constexpr int QF = D / 32;                   // products over the channels
   constexpr int OS = D + 4;                    // row stride of the waves' sums in LDS
   // Where Q's fragments are: in registers, or (256 bf16 channels, whose K, V and
@@ -243,7 +251,7 @@ __global__ __launch_bounds__(256, waves_for(D)) void attn_units_kernel(AttnArgs 
   u32x4 kf[2][KL];
   uint32_t vw[8][VW];
   f32x4 ks[2], vs[2];
-  const uint32_t koff = c16 * (D * E) + 16 * g, voff = 4 * g * (D * E) + c16 * (VC * E);
+  const uint32_t koff = c16 * (D * E) + 16 * g, voff = 4 * g * (D * E) + c16 * (VP * E);
   auto load_k = [&](const Half* hf) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -269,7 +277,7 @@ __global__ __launch_bounds__(256, waves_for(D)) void attn_units_kernel(AttnArgs 
         if constexpr (VW >= 4) {
 #pragma unroll
           for (int j = 0; j < VW / 4; ++j) {
-            const u32x4 w = once<u32x4>(src + 16 * j);
+            const u32x4 w = once<u32x4>(src + 256 * j);
             dst[4 * j] = w[0]; dst[4 * j + 1] = w[1]; dst[4 * j + 2] = w[2]; dst[4 * j + 3] = w[3];
           }
         }
@@ -341,7 +349,7 @@ __global__ __launch_bounds__(256, waves_for(D)) void attn_units_kernel(AttnArgs 
     const bool more = begin_unit();
     if (done) {
       // join the waves: O^T tile j, register i of lane (h, g) is channel
-      // VC (4 g + i) + j of head h
+      // 16 VP (j / VP) + VP (4 g + i) + j % VP of head h
       l = xor32_sum(xor16_sum(l));
       if (g == 0) { sm[wave][c16] = m; sl[wave][c16] = l; }
       if (c16 < nh_) {
@@ -349,30 +357,30 @@ __global__ __launch_bounds__(256, waves_for(D)) void attn_units_kernel(AttnArgs 
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int j = 0; j < VC; j += 4)
-            *(f32x4*)&so[wave][c16][VC * (4 * g + i) + j] = f32x4{o[j][i], o[j + 1][i], o[j + 2][i], o[j + 3][i]};
+            *(f32x4*)&so[wave][c16][16 * VP * (j / VP) + VP * (4 * g + i) + j % VP] =
+                f32x4{o[j][i], o[j + 1][i], o[j + 2][i], o[j + 3][i]};
       }
       __syncthreads();
-      for (int idx = threadIdx.x; idx < nh_ * D; idx += 256) {
-        const int h = idx / D, d = idx % D;
+      for (int idx = threadIdx.x; idx < nh_ * (D / 4); idx += 256) {
+        const int h = idx / (D / 4), td = idx % (D / 4);
         float M = sm[0][h];
 #pragma unroll
         for (int w = 1; w < kWaves; ++w) M = fmaxf(M, sm[w][h]);
-        float L = 0.f, y = 0.f;
+        float L = 0.f;
+        f32x4 y = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
           const float r = exp2_(sm[w][h] - M);
           L += sl[w][h] * r;
-          y += so[w][h][d] * r;
+          y += *(const f32x4*)&so[w][h][4 * td] * r;
         }
-        if (!whole_) {
+        if (whole_) {
+          put_row<D>(a, row0 + h, td, y, M, L);
+        } else {
           const int at = place_ * p.nh + h;
-          put<float>(p.part, (int64_t)at * D + d, y);
-          if (d == 0) put<u32x2>(p.ml, at, u32x2{__float_as_uint(M), __float_as_uint(L)});
-          continue;
+          put<f32x4>(p.part, (int64_t)at * (D / 4) + td, y);
+          if (td == 0) put<u32x2>(p.ml, at, u32x2{__float_as_uint(M), __float_as_uint(L)});
         }
-        const int64_t row = row0 + h;
-        put_out(a, row * D + d, L == 0.f ? 0.f : y / L);
-        if (d == 0) put_lse(a, row, M, L);
       }
       if (!more) return;
       __syncthreads();                         // the sums in LDS have been read
@@ -570,11 +578,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, Plan p, int 
       }
     }
     const int64_t row = (int64_t)b * a.hq + u / p.ht * p.G + h0 + h;
-    if (L == 0.f) y = f32x4{0.f, 0.f, 0.f, 0.f};
-    else y /= L;
-    if (a.out_bf16) put<u32x2>(a.out, (row * D >> 2) + td, u32x2{pack2(y[0], y[1]), pack2(y[2], y[3])});
-    else put<f32x4>(a.out, (row * D >> 2) + td, y);
-    if (td == 0) put_lse(a, row, M, L);
+    put_row<D>(a, row, td, y, M, L);
   }
   }
 }
@@ -592,7 +596,7 @@ Plan make_plan(const KvCache& c, int B, int hq, int max_len, int window) {
   // the tokens a sequence can span: a window begins anywhere in a step
   int64_t span = max_len;
   if (window && window + (int64_t)kStep - 1 < span) span = window + (int64_t)kStep - 1;
-  if (span > kDirect * kStep) p.wgs = 256 * waves_for(c.D);
+  if (span * c.D * (c.format == KV_BF16 ? 2 : 1) > kDirect) p.wgs = 256 * waves_for(c.D);
   return p;
 }
 
