@@ -59,8 +59,9 @@ __device__ __forceinline__ uint32_t codes2(uint32_t w) {
 //     by one step at most, whatever the sequences' lengths are. A workgroup finds
 //     its part from the lengths and writes a unit that it holds whole to the
 //     output, a unit's piece to the workspace: at most two, in its places 0 (its
-//     first unit) and 1 (its last). The second kernel joins the pieces of each
-//     unit in order.
+//     first unit) and 1 (its last). Whoever has a unit's first step notes where
+//     the first piece is and how many there are, and the second kernel joins the
+//     pieces of each unit in order.
 struct Plan {
   int wgs;
   int G, ht;             // query heads of a group, head tiles of 16 in it
@@ -69,6 +70,7 @@ struct Plan {
   uint32_t tpm;          // ceil(2^32 / (page_size / 16)): page of a 16-token tile by a high product
   float* part;           // [2 wgs][nh][D]
   float2* ml;            // [2 wgs][nh] maximum and sum
+  int2* cuts;            // [B][units] place of the first piece, number of pieces
 };
 // Direct against dealt with its second kernel, us a pass: K of 128 KB (1 x 1000
 // fp8) 12.7 / 17.0, 192 KB (1 x 1500; 64 x 1500) 13.8 / 16.9; 27.9 / 31.6,
@@ -193,12 +195,14 @@ __global__ __launch_bounds__(256, waves_for(D)) void attn_units_kernel(AttnArgs 
   // in all. What steers the loops has to be uniform for the compiler too: as lane
   // values they cost 40 spilled registers (2 x 131071 int8: 150 us)
   int b, u, v = 0, left = 1, place = 0;
+  uint32_t start = 0;                          // where the unit begins in the row of all
+  Cut cut(1, 1);
   if (DEALT) {
     const int per = (a.B + 255) / 256;
     uint32_t all;
     uint32_t at = cost_before(a, per, &all, scan);
     all *= p.units;
-    const Cut cut(all, p.wgs);
+    cut = Cut(all, p.wgs);
     // neighbouring parts on one XCD (workgroups go to the eight in turn): head
     // tiles of one key/value head then meet in its L2
     const uint32_t run = (cut.parts + 7) >> 3, rank = (blockIdx.x & 7) * run + (blockIdx.x >> 3);
@@ -222,6 +226,7 @@ __global__ __launch_bounds__(256, waves_for(D)) void attn_units_kernel(AttnArgs 
     const int n = span_of(a, uniform(a.lens, b)).cost();
     u = in / n;
     v = in - u * n;
+    start = x - v;
   } else {
     b = blockIdx.x / p.units;
     u = blockIdx.x % p.units;
@@ -301,6 +306,11 @@ __global__ __launch_bounds__(256, waves_for(D)) void attn_units_kernel(AttnArgs 
       left -= sp.steps + kExtra - v;
       v = 0;
       if (r1 <= r0) return false;
+      start += sp.steps + kExtra;
+      if (r0 == 0) {
+        const int pieces = r1 == sp.steps ? 1 : (int)cut.part_of(start - 1) - (place >> 1) + 1;
+        if (threadIdx.x == 0) put<u32x2>(p.cuts, (int64_t)b * p.units + u, u32x2{(uint32_t)place, (uint32_t)pieces});
+      }
     } else {
       left = 0;
     }
@@ -513,31 +523,16 @@ __global__ __launch_bounds__(256, waves_for(D)) void attn_units_kernel(AttnArgs 
 template <int D, bool ROWS>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, Plan p, int groups) {
   constexpr int TG = 256 / (D / 4);            // thread groups
-  __shared__ uint32_t scan[kWaves + 1];
   __shared__ f32x4 so[TG][D / 4];
   __shared__ float sm[TG], sl[TG];
   const int b = (int)(blockIdx.x / groups), group = (int)(blockIdx.x % groups);
-  const int per = (a.B + 255) / 256;
-  uint32_t all;
-  uint32_t at = cost_before(a, per, &all, scan);
-  for (int i = 0; i < per; ++i) {
-    const int bb = threadIdx.x * per + i;
-    if (bb == b) scan[kWaves] = at;
-    if (bb < a.B) at += span_of(a, a.lens[bb]).cost();
-  }
-  __syncthreads();
-  const uint32_t n = span_of(a, uniform(a.lens, b)).cost(), xb = scan[kWaves] * p.units;
-  const Cut cut(all * p.units, p.wgs);
+  const bool some = span_of(a, uniform(a.lens, b)).steps > 0;
   const int tg = threadIdx.x / (D / 4), td = threadIdx.x % (D / 4);
   for (int u = ROWS ? group / p.nh : group; u < p.units; u += ROWS ? p.units : groups) {
-  const uint32_t x0 = xb + u * n;
-  int w0 = 0, pieces = 0, place0 = 0;
-  if (n) {
-    w0 = cut.part_of(x0 + kExtra);             // the part of its first step
-    pieces = cut.part_of(x0 + n - 1) - w0 + 1;
-    if (pieces == 1) continue;                 // written whole by its workgroup
-    place0 = 2 * w0 + (x0 > cut.start(w0) ? 1 : 0);     // the first piece ends its workgroup's part
-  }
+  const int64_t unit = (int64_t)b * p.units + u;
+  const int place0 = uniform((const int*)p.cuts, 2 * unit);
+  const int pieces = some ? uniform((const int*)p.cuts, 2 * unit + 1) : 0;
+  if (pieces == 1) continue;                   // written whole by its workgroup
   const int h0 = u % p.ht * 16, nh = min(16, p.G - h0);
   for (int h = ROWS ? group % p.nh : tg; h < nh; h += ROWS ? nh : TG) {
     float M = kLowest, L = 0.f;
@@ -550,7 +545,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, Plan p, int 
       for (int k = 0; k < 4; ++k) {
         const int j = i + k * (ROWS ? TG : 1);
         if (j < pieces) {
-          const int q = (j == 0 ? place0 : 2 * (w0 + j)) * p.nh + h;
+          const int q = (j == 0 ? place0 : 2 * ((place0 >> 1) + j)) * p.nh + h;
           ml[k] = p.ml[q];
           v[k] = *(const f32x4*)(p.part + (int64_t)q * D + 4 * td);
         }
@@ -615,7 +610,6 @@ hipError_t run(const AttnArgs& a, const Plan& p, hipStream_t s) {
     const int groups = p.units * p.nh;         // eight pieces a unit and more
     attn_join_kernel<D, true><<<(unsigned)(a.B * groups), 256, 0, s>>>(a, p, groups);
   } else {
-    // every workgroup adds up all the lengths: the more sequences, the fewer groups
     const int groups = std::min(p.units, std::max(1, 4096 / a.B));
     attn_join_kernel<D, false><<<(unsigned)(a.B * groups), 256, 0, s>>>(a, p, groups);
   }
@@ -634,13 +628,15 @@ hipError_t run_d(const AttnArgs& a, const Plan& p, hipStream_t s) {
 size_t attn_workspace_bytes(const KvCache& c, int B, int hq, int max_len, int window) {
   const Plan p = make_plan(c, B, hq, max_len, window);
   const size_t n = (size_t)2 * p.wgs * p.nh;
-  return align256(n * c.D * 4) + align256(n * 8);
+  return p.wgs ? align256(n * c.D * 4) + align256(n * 8) + align256((size_t)B * p.units * 8) : 0;
 }
 
 hipError_t launch_attn_decode(const AttnArgs& a, hipStream_t s) {
   Plan p = make_plan(a.c, a.B, a.hq, a.max_len, a.window);
   p.part = a.ws;
-  p.ml = (float2*)((char*)a.ws + align256((size_t)2 * p.wgs * p.nh * a.c.D * 4));
+  const size_t n = (size_t)2 * p.wgs * p.nh;
+  p.ml = (float2*)((char*)a.ws + align256(n * a.c.D * 4));
+  p.cuts = (int2*)((char*)p.ml + align256(n * 8));
   if (a.c.format == KV_BF16) return run_d<KV_BF16>(a, p, s);
   if (a.c.format == KV_E4M3) return run_d<KV_E4M3>(a, p, s);
   return run_d<KV_INT8>(a, p, s);
