@@ -404,7 +404,7 @@ int lcp_deploy_forward(const void* vals, const uint32_t* meta,
  * the results are the same.
  *
  * Index arrays (positions, slots, page numbers, lengths) are int32 in device
- * memory; entries outside their range never cause an access outside a buffer:
+ * memory (4-byte aligned); entries outside their range never cause an access outside a buffer:
  * each entry point says what it does with them.
  */
 typedef struct lcp_heads {
@@ -510,8 +510,9 @@ int lcp_kv_read(const lcp_kv_cache* c, const int32_t* slots, int T, void* k_out,
  *   out = sum exp(z_t - m) v_t / l,  lse = m + ln l.
  * A sequence without tokens gives out 0 and lse -inf. What the cache holds in
  * other slots (the rest of a last page, freed pages) has no effect, whatever
- * its bits. The sums are fp32; the work is split over the tokens and joined in
- * a fixed order, so equal inputs give equal bits.
+ * its bits; a NaN or an infinity among the counted tokens' values shows in the
+ * rows that use it as NaN or infinity. The sums are fp32; the work is split over
+ * the tokens and joined in a fixed order, so equal inputs give equal bits.
  *   q: bf16 [B][hq][D] with q_row elements between sequences (>= hq D), heads
  *   adjacent, 16-byte aligned rows; hq a multiple of heads.
  *   pages: [B][max_pages], the page number of tokens page_size i ..; entries

@@ -4,9 +4,8 @@
 //
 // Every cached element is used by the G query heads of its group only (2 G
 // flops a byte with 8-bit codes), so the bytes of K and V bound the operator.
-// One pass over them with the running maximum and sum of the softmax; a
-// workgroup takes a chunk of one sequence's tokens for one key/value head and
-// (up to 16 of) its query heads, and chunks are joined by a second kernel.
+// They are read once, with the running maximum and sum of the softmax; many
+// workgroups share a long sequence and a second kernel joins their sums.
 //
 // A wave takes 32 tokens at a time and keeps everything in registers, from the
 // loads to the matrix instructions (16x16x32 bf16, fp32 sums):
@@ -15,12 +14,23 @@
 //     channels meet in one product does not matter as long as Q's fragment
 //     holds the same ones.
 //   The result leaves lane (h, g) with tokens 4g .. 4g+3 of each half of the 32
-//   for head h: a softmax over registers, no exchange between lanes except for
-//   a new maximum.
+//     for head h: a softmax over registers, no exchange between lanes except
+//     for a new maximum.
 //   O^T[channel][head] += V^T P^T   B = P as it stands in the registers: lane
 //     (h, g) supplies K slots 8g .. 8g+7, which are the tokens named above. So
-//     lane (c, g) loads those eight tokens' channels c D/16 .. of V, and the
+//     lane (c, g) loads those eight tokens' channels VP c .. of V, and the
 //     transposition is a byte permutation within the lane.
+// 8-bit codes become bf16 exactly; their scales multiply the scores and the
+// weights. Groups of fewer than 16 heads leave columns of the products empty,
+// which costs nothing while the bytes bound it; groups of more read K and V once
+// for every 16 heads, from the L2 when the workgroups meet there.
+//
+// Measured (us; bytes of K, V and scales over time), 64 heads in 8 groups of 128
+// channels unless said: 128 sequences up to 8192, bf16, 2.15 GB 340 (6.3 TB/s);
+// 2 x 131071 int8, 32 heads, 448 MB 80 (5.6); 48 up to 4096 fp8, 203 MB 45 (4.6);
+// 24 windows of 4096, 16 heads of 256, bf16, 345 MB 68 (5.1); 1 x 333 bf16, 32
+// heads of their own, 11.7, of which 7 on the GPU. One workgroup a query head, a
+// wave a token, took 11830, 58755, 2861, 4036 and 92.
 #include <algorithm>
 
 #include "serve.h"
@@ -76,8 +86,12 @@ struct Plan {
 // fp8) 12.7 / 17.0, 192 KB (1 x 1500; 64 x 1500) 13.8 / 16.9; 27.9 / 31.6,
 // 256 KB (1 x 2000; 8 x 1000 bf16) 18.1 / 17.0; 17.4 / 16.8.
 constexpr int kDirect = 192 << 10;
-constexpr uint32_t kLeast = 12;     // steps of a part, where there are fewer than wgs such parts
+// Cost of beginning and ending a unit, in steps: 2, 4, 8, 12 gave 53.1, 46.9, 46.4,
+// 47.7 us at 48 x 4096 fp8 and 56.5, 51.4, 50.0, 51.4 at 96 x 2048.
 constexpr int kExtra = 8;
+// Cost of a part at least, where that makes fewer than wgs: 9, 12, 16, 24 gave 20.2,
+// 16.3, 17.5, 20.6 us at 8 x 2000 bf16 and 18.2, 17.7, 18.1, 17.6 at 2 x 3000.
+constexpr uint32_t kLeast = 12;
 
 // The cut of `all` steps.
 struct Cut {
@@ -95,8 +109,8 @@ struct Cut {
 };
 
 // An index array entry at an address that is the same for the whole wave, read
-// through the scalar cache (the arrays are inputs, which no kernel writes): it
-// does not queue behind the loads of K and V, which return in order.
+// through the scalar cache (the kernel that reads it does not write it): it does
+// not queue behind the loads of K and V, which return in order.
 __device__ __forceinline__ int uniform(const int* p, int64_t i) {
   typedef const int __attribute__((address_space(4))) * ConstPtr;
   return ((ConstPtr)(uintptr_t)p)[i];
@@ -307,10 +321,6 @@ __global__ __launch_bounds__(256, waves_for(D)) void attn_units_kernel(AttnArgs 
       v = 0;
       if (r1 <= r0) return false;
       start += sp.steps + kExtra;
-      if (r0 == 0) {
-        const int pieces = r1 == sp.steps ? 1 : (int)cut.part_of(start - 1) - (place >> 1) + 1;
-        if (threadIdx.x == 0) put<u32x2>(p.cuts, (int64_t)b * p.units + u, u32x2{(uint32_t)place, (uint32_t)pieces});
-      }
     } else {
       left = 0;
     }
@@ -345,6 +355,10 @@ __global__ __launch_bounds__(256, waves_for(D)) void attn_units_kernel(AttnArgs 
     __builtin_amdgcn_sched_barrier(0);         // K before V, for the same reason
     load_v(cur);
     __builtin_amdgcn_sched_barrier(0);
+    if (DEALT && r0 == 0 && threadIdx.x == 0) {
+      const uint32_t pieces = whole ? 1 : cut.part_of(start - 1) - (place >> 1) + 1;
+      put<u32x2>(p.cuts, (int64_t)b * p.units + u, u32x2{(uint32_t)place, pieces});
+    }
     return true;
   };
 
@@ -523,58 +537,54 @@ __global__ __launch_bounds__(256, waves_for(D)) void attn_units_kernel(AttnArgs 
 template <int D, bool ROWS>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, Plan p, int groups) {
   constexpr int TG = 256 / (D / 4);            // thread groups
+  constexpr int STEP = ROWS ? TG : 1;          // from a thread group's piece to its next
   __shared__ f32x4 so[TG][D / 4];
   __shared__ float sm[TG], sl[TG];
   const int b = (int)(blockIdx.x / groups), group = (int)(blockIdx.x % groups);
   const bool some = span_of(a, uniform(a.lens, b)).steps > 0;
   const int tg = threadIdx.x / (D / 4), td = threadIdx.x % (D / 4);
+  const auto add = [](float& M, float& L, f32x4& y, float m, float l, f32x4 v) {
+    const float mn = fmaxf(M, m), r0 = exp2_(M - mn), r1 = exp2_(m - mn);
+    L = L * r0 + l * r1;
+    y = y * r0 + v * r1;
+    M = mn;
+  };
   for (int u = ROWS ? group / p.nh : group; u < p.units; u += ROWS ? p.units : groups) {
-  const int64_t unit = (int64_t)b * p.units + u;
-  const int place0 = uniform((const int*)p.cuts, 2 * unit);
-  const int pieces = some ? uniform((const int*)p.cuts, 2 * unit + 1) : 0;
-  if (pieces == 1) continue;                   // written whole by its workgroup
-  const int h0 = u % p.ht * 16, nh = min(16, p.G - h0);
-  for (int h = ROWS ? group % p.nh : tg; h < nh; h += ROWS ? nh : TG) {
-    float M = kLowest, L = 0.f;
-    f32x4 y = {0.f, 0.f, 0.f, 0.f};
-    for (int i = ROWS ? tg : 0; i < pieces; i += 4 * (ROWS ? TG : 1)) {
-      // four pieces' loads together, then one after the other
-      f32x4 v[4];
-      float2 ml[4];
+    const int64_t unit = (int64_t)b * p.units + u;
+    const int place0 = uniform((const int*)p.cuts, 2 * unit);
+    const int pieces = some ? uniform((const int*)p.cuts, 2 * unit + 1) : 0;
+    if (pieces == 1) continue;                 // written whole by its workgroup
+    const int h0 = u % p.ht * 16, nh = min(16, p.G - h0);
+    for (int h = ROWS ? group % p.nh : tg; h < nh; h += ROWS ? nh : TG) {
+      float M = kLowest, L = 0.f;
+      f32x4 y = {0.f, 0.f, 0.f, 0.f};
+      for (int i = ROWS ? tg : 0; i < pieces; i += 4 * STEP) {
+        // four pieces' loads together, then one after the other
+        f32x4 v[4];
+        float2 ml[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int j = i + k * (ROWS ? TG : 1);
-        if (j < pieces) {
-          const int q = (j == 0 ? place0 : 2 * ((place0 >> 1) + j)) * p.nh + h;
-          ml[k] = p.ml[q];
-          v[k] = *(const f32x4*)(p.part + (int64_t)q * D + 4 * td);
+        for (int k = 0; k < 4; ++k) {
+          const int j = i + k * STEP;
+          if (j < pieces) {
+            // the first piece ends its workgroup's part, the others begin theirs
+            const int q = (j == 0 ? place0 : 2 * ((place0 >> 1) + j)) * p.nh + h;
+            ml[k] = p.ml[q];
+            v[k] = *(const f32x4*)(p.part + (int64_t)q * D + 4 * td);
+          }
         }
-      }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (i + k * (ROWS ? TG : 1) < pieces) {
-          const float mn = fmaxf(M, ml[k].x), r0 = exp2_(M - mn), r1 = exp2_(ml[k].x - mn);
-          L = L * r0 + ml[k].y * r1;
-          y = y * r0 + v[k] * r1;
-          M = mn;
-        }
+        for (int k = 0; k < 4; ++k)
+          if (i + k * STEP < pieces) add(M, L, y, ml[k].x, ml[k].y, v[k]);
       }
-    }
-    if (ROWS) {
-      so[tg][td] = y;
-      if (td == 0) { sm[tg] = M; sl[tg] = L; }
-      __syncthreads();
-      if (tg != 0) return;
-      for (int w = 1; w < TG; ++w) {
-        const float mn = fmaxf(M, sm[w]), r0 = exp2_(M - mn), r1 = exp2_(sm[w] - mn);
-        L = L * r0 + sl[w] * r1;
-        y = y * r0 + so[w][td] * r1;
-        M = mn;
+      if (ROWS) {
+        so[tg][td] = y;
+        if (td == 0) { sm[tg] = M; sl[tg] = L; }
+        __syncthreads();
+        if (tg != 0) return;
+        for (int w = 1; w < TG; ++w) add(M, L, y, sm[w], sl[w], so[w][td]);
       }
+      put_row<D>(a, (int64_t)b * a.hq + u / p.ht * p.G + h0 + h, td, y, M, L);
     }
-    const int64_t row = (int64_t)b * a.hq + u / p.ht * p.G + h0 + h;
-    put_row<D>(a, row, td, y, M, L);
-  }
   }
 }
 
@@ -598,7 +608,6 @@ Plan make_plan(const KvCache& c, int B, int hq, int max_len, int window) {
 template <int FMT, int D>
 hipError_t run(const AttnArgs& a, const Plan& p, hipStream_t s) {
   const int64_t units = (int64_t)a.B * p.units;
-  if (units * p.nh > 0x7fffffff) return hipErrorInvalidValue;
   if (p.wgs == 0) {
     attn_units_kernel<FMT, D, false><<<(unsigned)units, 256, 0, s>>>(a, p);
     return hipGetLastError();

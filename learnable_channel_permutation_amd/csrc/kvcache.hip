@@ -262,7 +262,6 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvCache c, const int* slot
 template <int FMT, int D>
 hipError_t run_append(const KvAppendArgs& a, hipStream_t s) {
   const int64_t rows = (int64_t)a.T * (a.q.heads + 2 * a.c.heads), n = rows * (D / 16), grid = (n + 255) / 256;
-  if (grid > 0x7fffffff) return hipErrorInvalidValue;
   const int64_t q = (int64_t)a.T * a.q.heads * D * 4, kv = (int64_t)a.T * a.c.heads * 2 * D * (FMT == KV_BF16 ? 4 : 3);
   if (q + kv > kStreamBytes) kv_append_kernel<FMT, D, true><<<(unsigned)grid, 256, 0, s>>>(a, n);
   else kv_append_kernel<FMT, D, false><<<(unsigned)grid, 256, 0, s>>>(a, n);
@@ -279,7 +278,6 @@ hipError_t run_append_d(const KvAppendArgs& a, hipStream_t s) {
 template <int FMT, bool BF>
 hipError_t run_read(const KvCache& c, const int* slots, int T, void* k, void* v, hipStream_t s) {
   const int64_t n = (int64_t)T * c.heads * (c.D / 8), grid = (n + 255) / 256;
-  if (grid > 0x7fffffff) return hipErrorInvalidValue;
   const bool stream = n * 16 * ((FMT == KV_BF16 ? 2 : 1) + (BF ? 2 : 4)) > kStreamBytes;
   if (stream) kv_read_kernel<FMT, BF, true><<<(unsigned)grid, 256, 0, s>>>(c, slots, n, (char*)k, (char*)v);
   else kv_read_kernel<FMT, BF, false><<<(unsigned)grid, 256, 0, s>>>(c, slots, n, (char*)k, (char*)v);

@@ -11,6 +11,7 @@ using namespace lcp;
 namespace {
 
 inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+inline bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }      // index arrays
 inline hipStream_t S(void* s) { return reinterpret_cast<hipStream_t>(s); }
 constexpr int64_t kMaxStride = (int64_t)1 << 40;   // keeps every element offset far inside 64 bits
 
@@ -54,7 +55,7 @@ int check_attn_sizes(const lcp_kv_cache* c, int B, int hq, int max_len, int wind
   if ((int64_t)B * hq * c->D >= ((int64_t)1 << 31) || max_len >= (1 << 28)) return LCP_E_INVAL;
   // steps of 32 tokens over all sequences and head tiles in 32 bits
   const int64_t units = (int64_t)B * c->heads * ((hq / c->heads + 15) / 16);
-  if (units * ((int64_t)max_len / 32 + 8) >= ((int64_t)1 << 31)) return LCP_E_INVAL;
+  if (units * ((int64_t)max_len / 32 + 10) >= ((int64_t)1 << 31)) return LCP_E_INVAL;
   return LCP_OK;
 }
 
@@ -107,7 +108,10 @@ int lcp_rope(const lcp_heads* q, const lcp_heads* k, lcp_dtype dt, int T, int D,
     if (!good_rows_in(h) || !good_rows_out(h, T, D)) return LCP_E_INVAL;
     if (((uintptr_t)h->x & es) != 0 || ((uintptr_t)h->y & es) != 0) return LCP_E_INVAL;
   }
-  if ((int64_t)T * (q->heads + (k ? k->heads : 0)) >= ((int64_t)1 << 31)) return LCP_E_INVAL;
+  // rows and grids in 32 bits
+  const int64_t rows = (int64_t)T * (q->heads + (k ? k->heads : 0));
+  if (rows >= ((int64_t)1 << 31) || rows * D >= ((int64_t)1 << 38)) return LCP_E_INVAL;
+  if (!aligned4(pos)) return LCP_E_INVAL;
   RopeArgs a{};
   a.q = rows_of(q);
   if (k) a.k = rows_of(k);
@@ -125,7 +129,7 @@ int lcp_kv_append(const lcp_kv_cache* c, const lcp_heads* q, const lcp_heads* k,
   KvAppendArgs a{};
   int rc = check_cache(c, &a.c);
   if (rc != LCP_OK) return rc;
-  if (!k || !v || !slots || T <= 0) return LCP_E_INVAL;
+  if (!k || !v || !slots || T <= 0 || !aligned4(slots)) return LCP_E_INVAL;
   if (!good_rows_in(k) || !good_rows_in(v) || k->heads != c->heads || v->heads != c->heads) return LCP_E_INVAL;
   if (((uintptr_t)k->x & 1) != 0 || ((uintptr_t)v->x & 1) != 0) return LCP_E_INVAL;
   if (q) {
@@ -133,7 +137,7 @@ int lcp_kv_append(const lcp_kv_cache* c, const lcp_heads* q, const lcp_heads* k,
     if (((uintptr_t)q->x & 1) != 0 || ((uintptr_t)q->y & 1) != 0) return LCP_E_INVAL;
   }
   if (table) {
-    if (!pos || max_pos <= 0 || !aligned16(table) || rot_dim <= 0 || rot_dim > c->D) return LCP_E_INVAL;
+    if (!pos || max_pos <= 0 || !aligned4(pos) || !aligned16(table) || rot_dim <= 0 || rot_dim > c->D) return LCP_E_INVAL;
     if (interleaved != 0 && interleaved != 1) return LCP_E_INVAL;
     if (rot_dim % 16 != 0) return LCP_E_UNSUPPORTED;
   }
@@ -157,7 +161,7 @@ int lcp_kv_read(const lcp_kv_cache* c, const int32_t* slots, int T, void* k_out,
   KvCache kc;
   int rc = check_cache(c, &kc);
   if (rc != LCP_OK) return rc;
-  if (!slots || T <= 0 || !k_out || !v_out || k_out == v_out) return LCP_E_INVAL;
+  if (!slots || T <= 0 || !aligned4(slots) || !k_out || !v_out || k_out == v_out) return LCP_E_INVAL;
   if (odt != LCP_F32 && odt != LCP_BF16) return LCP_E_UNSUPPORTED;
   if (!aligned16(k_out) || !aligned16(v_out)) return LCP_E_INVAL;
   if ((int64_t)T * c->heads >= ((int64_t)1 << 31) / 32) return LCP_E_INVAL;
@@ -182,7 +186,7 @@ int lcp_attn_decode(const lcp_kv_cache* c, const void* q, int64_t q_row, int B, 
   AttnArgs a{};
   int rc = check_cache(c, &a.c);
   if (rc != LCP_OK) return rc;
-  if (!q || !pages || !lens || !out || max_pages <= 0) return LCP_E_INVAL;
+  if (!q || !pages || !lens || !out || max_pages <= 0 || !aligned4(pages) || !aligned4(lens)) return LCP_E_INVAL;
   rc = check_attn_sizes(c, B, hq, max_len, window);
   if (rc != LCP_OK) return rc;
   if (odt != LCP_F32 && odt != LCP_BF16) return LCP_E_UNSUPPORTED;

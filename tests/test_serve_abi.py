@@ -50,7 +50,7 @@ def test_rope_refusals():
                 dict(q=_rows(L, heads=0)), dict(q=_rows(L, x=0)), dict(q=_rows(L, y=0)), dict(q=_rows(L, x=P + 1)),
                 dict(q=_rows(L, xt=-512)), dict(q=_rows(L, yt=500)), dict(q=_rows(L, yh=127)), dict(q=_rows(L, yt=0)),
                 dict(q=_rows(L, x=P, y=P, xt=1024)), dict(k=_rows(L, x=0)), dict(k=_rows(L, yt=100)),
-                dict(dt=L.LCP_F32, q=_rows(L, x=P + 2)), dict(q=_rows(L, xt=1 << 50))):
+                dict(dt=L.LCP_F32, q=_rows(L, x=P + 2)), dict(q=_rows(L, xt=1 << 50)), dict(pos=P + 2)):
         assert call(**bad) == L.LCP_E_INVAL, bad
     assert call(dt=7) == L.LCP_E_UNSUPPORTED
     assert call(D=1026, rot=64, q=_rows(L, yt=1 << 20, yh=1 << 11)) == L.LCP_E_UNSUPPORTED
@@ -89,7 +89,7 @@ def test_append_and_read_refusals():
         r = lambda x: None if x is None else ctypes.byref(x)       # noqa: E731
         return L.LIB.lcp_kv_append(r(c or _cache(L)), r(q), r(k), r(v), T, slots, table, n, pos, rot, inter, None)
 
-    for bad in (dict(k=None), dict(v=None), dict(T=0), dict(slots=None), dict(k=_rows(L, heads=3)),
+    for bad in (dict(k=None), dict(v=None), dict(T=0), dict(slots=None), dict(slots=P + 2), dict(pos=P + 1), dict(k=_rows(L, heads=3)),
                 dict(v=_rows(L, heads=5)), dict(k=_rows(L, x=P + 1)), dict(v=_rows(L, x=0)), dict(pos=None), dict(n=0),
                 dict(rot=0), dict(rot=144), dict(inter=3), dict(table=P + 4), dict(q=_rows(L, y=0)),
                 dict(q=_rows(L), table=None), dict(q=_rows(L, yt=100))):
@@ -116,7 +116,7 @@ def test_attend_refusals():
     for bad in (dict(q=None), dict(q=P + 8), dict(row=504), dict(row=516), dict(B=0), dict(hq=0), dict(hq=6),
                 dict(pages=None), dict(mp=0), dict(lens=None), dict(ml=-1), dict(ml=161), dict(scale=math.nan),
                 dict(scale=math.inf), dict(window=-1), dict(out=None), dict(out=P + 4), dict(lse=P + 2),
-                dict(B=1 << 23), dict(ml=16000, mp=1000, ws=None)):
+                dict(pages=P + 1), dict(lens=P + 2), dict(B=1 << 23), dict(ml=16000, mp=1000, ws=None)):
         assert call(**bad) == L.LCP_E_INVAL, bad
     assert call(odt=4) == L.LCP_E_UNSUPPORTED
     c = _cache(L)
