@@ -155,27 +155,28 @@ class PagedKVCache:
 
     def read(self, slots, k_out=None, v_out=None, stream=None):
         """The stored k and v of slots, [T, heads, D] bfloat16 unless outputs are given (lcp_kv_read)."""
-        shape = (slots.shape[0], self.c.heads, self.c.D)
-        if k_out is None:
-            k_out = _used_on(stream, slots.new_empty(shape, dtype=torch.bfloat16))
-        if v_out is None:
+        if stream is not None and k_out is None:
+            k_out = _used_on(stream, slots.new_empty((slots.shape[0], self.c.heads, self.c.D), dtype=torch.bfloat16))
+        if stream is not None and v_out is None:
             v_out = _used_on(stream, torch.empty_like(k_out))
-        lcp_kv_read(self.c, slots, k_out, v_out, stream)
+        code, k_out, v_out = _lib._serve.read(self.c, slots, k_out, v_out, stream)
+        _lib._check("lcp_kv_read", code)
         return k_out, v_out
 
     def attend(self, q, pages, lens, max_len=None, scale=None, window=0, out=None, lse=None, ws=None, stream=None):
         """Attention of one new token of each sequence, q [B, hq, D] bfloat16 (lcp_attn_decode): (out, lse). max_len,
         the host's bound on lens, defaults to what the page table can hold; scale to D^-1/2."""
-        B, hq, _ = q.shape
-        if max_len is None:
-            max_len = pages.shape[1] * self.c.page_size
-        if out is None:
-            out = _used_on(stream, torch.empty_like(q, memory_format=torch.contiguous_format))
-        if lse is None:
-            lse = _used_on(stream, q.new_empty((B, hq), dtype=torch.float32))
-        if ws is None:
-            n = lcp_attn_decode_workspace_bytes(self.c, B, hq, max_len, window)
-            if n:
-                ws = _used_on(stream, q.new_empty(n, dtype=torch.uint8))
-        lcp_attn_decode(self.c, q, pages, lens, max_len, out, ws, lse, scale, window, stream)
+        if stream is not None:
+            if max_len is None:
+                max_len = pages.shape[1] * self.c.page_size
+            if out is None:
+                out = _used_on(stream, torch.empty_like(q, memory_format=torch.contiguous_format))
+            if lse is None:
+                lse = _used_on(stream, q.new_empty(q.shape[:2], dtype=torch.float32))
+            if ws is None:
+                n = lcp_attn_decode_workspace_bytes(self.c, q.shape[0], q.shape[1], max_len, window)
+                ws = _used_on(stream, q.new_empty(n, dtype=torch.uint8)) if n else None
+        code, out, lse = _lib._serve.attend(self.c, q, pages, lens, max_len, out, lse, ws, scale, window, True,
+                                            stream)
+        _lib._check("lcp_attn_decode", code)
         return out, lse

@@ -1,6 +1,7 @@
 """ctypes binding of liblcp.so (the C ABI in include/lcp.h).
 
-Argument marshalling only: tensors become device pointers, dtypes become
+Argument marshalling only, for the serving calls by the native module _serve
+(csrc/bind.cpp), for the others here: tensors become device pointers, dtypes become
 lcp_dtype codes, the current torch stream becomes the HIP stream; every step
 of the computation runs in the library's kernels. A non-zero status raises
 LcpError. If the shared library is missing this module raises at import:
@@ -10,7 +11,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
 
 import torch
 
@@ -132,9 +132,9 @@ def _load():
         "lcp_sparse_gemm": (i, [vp, vp, vp, i, i, i, vp, vp]),
         "lcp_deploy_forward": (i, [vp, vp, vp, i, vp, i, i, i, vp, vp, vp]),
         "lcp_rope_table": (i, [ctypes.POINTER(lcp_rope_cfg), i, vp, vp]),
-        # head rows (vp): an lcp_heads by reference, or its bytes
-        "lcp_rope": (i, [vp, vp, i, i, i, vp, i, vp, i, i, i, vp]),
-        "lcp_kv_append": (i, [ctypes.POINTER(lcp_kv_cache), vp, vp, vp, i, vp, vp, i, vp, i, i, vp]),
+        "lcp_rope": (i, [ctypes.POINTER(lcp_heads), ctypes.POINTER(lcp_heads), i, i, i, vp, i, vp, i, i, i, vp]),
+        "lcp_kv_append": (i, [ctypes.POINTER(lcp_kv_cache), ctypes.POINTER(lcp_heads), ctypes.POINTER(lcp_heads),
+                              ctypes.POINTER(lcp_heads), i, vp, vp, i, vp, i, i, vp]),
         "lcp_kv_read": (i, [ctypes.POINTER(lcp_kv_cache), vp, i, vp, vp, i, vp]),
         "lcp_attn_decode_workspace_bytes": (i, [ctypes.POINTER(lcp_kv_cache), i, i, i, i, psz]),
         "lcp_attn_decode": (i, [ctypes.POINTER(lcp_kv_cache), vp, ctypes.c_int64, i, i, vp, i, vp, i, f, i, vp, i, vp,
@@ -153,6 +153,7 @@ def _load():
 
 
 LIB = _load()
+from . import _serve  # noqa: E402  (built beside liblcp.so, which it calls; needs torch imported)
 
 _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
@@ -362,46 +363,7 @@ def lcp_deploy_forward(vals, meta, perm, B, X, cout, Xp, Y, stream=None):
 
 
 # ---- serving operators --------------------------------------------------------
-_KV_FORMATS = {torch.bfloat16: LCP_KV_BF16, torch.float8_e4m3fn: LCP_KV_E4M3, torch.int8: LCP_KV_INT8}
-_I32, _BF16, _F32 = torch.int32, torch.bfloat16, torch.float32
-
-
-def _index(t, n, name):
-    """A device int32 index array of n entries."""
-    if t.dtype is not _I32 or t.shape != (n,) or not t.is_contiguous():
-        raise ValueError("%s must be contiguous int32 of shape (%d,)" % (name, n))
-    return t.data_ptr()
-
-
-# the layout of lcp_heads; packing it takes a quarter of the time of filling the ctypes structure
-_pack_heads = struct.Struct("PPi4xqqqq").pack
-
-
-def _heads(x, y, D, dtype, name):
-    """Head rows [T, heads, D] (any strides, channels contiguous) as the bytes of an lcp_heads."""
-    shape = x.shape
-    if len(shape) != 3 or shape[2] != D or x.dtype is not dtype:
-        raise ValueError("%s must be [T, heads, %d] %s" % (name, D, dtype))
-    st, sh, one = x.stride()
-    yone = 1
-    if y is None:
-        yp = yt = yh = 0
-    else:
-        if y.shape != shape or y.dtype is not dtype:
-            raise ValueError("the output of %s must have its shape and dtype" % name)
-        yp = y.data_ptr()
-        yt, yh, yone = y.stride()
-    if one != 1 or yone != 1:
-        raise ValueError("the channels of %s must be contiguous" % name)
-    return _pack_heads(x.data_ptr(), yp, shape[1], st, sh, yt, yh)
-
-
-def _table(table):
-    """A rotary table [max_pos, rot_dim / 2, 2] -> (pointer, max_pos, rot_dim)."""
-    shape = table.shape
-    if len(shape) != 3 or shape[2] != 2 or table.dtype is not _F32 or not table.is_contiguous():
-        raise ValueError("table must be contiguous float32 [max_pos, rot_dim / 2, 2]")
-    return table.data_ptr(), shape[0], 2 * shape[1]
+_serve.use_streams(_stream)
 
 
 def make_rope_cfg(rot_dim, base=10000.0, scaling="none", factor=1.0, orig_len=0.0, low_turns=1.0, high_turns=32.0,
@@ -412,77 +374,28 @@ def make_rope_cfg(rot_dim, base=10000.0, scaling="none", factor=1.0, orig_len=0.
 
 
 def lcp_rope_table(cfg, table, stream=None):
-    p, max_pos, rot = _table(table)
-    if rot != cfg.rot_dim:
-        raise ValueError("table holds %d rotated channels, the configuration %d" % (rot, cfg.rot_dim))
-    return _check("lcp_rope_table", LIB.lcp_rope_table(ctypes.byref(cfg), max_pos, p, _stream(stream)))
+    if tuple(table.shape[1:]) != (cfg.rot_dim // 2, 2) or table.dtype != torch.float32 or not table.is_contiguous():
+        raise ValueError("table must be contiguous float32 [max_pos, %d, 2]" % (cfg.rot_dim // 2))
+    return _check("lcp_rope_table", LIB.lcp_rope_table(ctypes.byref(cfg), table.shape[0], _p(table), _stream(stream)))
 
 
 def lcp_rope(q, q_out, table, pos, k=None, k_out=None, interleaved=False, inverse=False, stream=None):
-    T, _, D = q.shape
-    dtype = q.dtype
-    hq = _heads(q, q_out, D, dtype, "q")
-    hk = None
-    if k is not None:
-        if k.shape[0] != T or k_out is None:
-            raise ValueError("k needs q's number of tokens and an output")
-        hk = _heads(k, k_out, D, dtype, "k")
-    p, max_pos, rot = _table(table)
-    code = LIB.lcp_rope(hq, hk, dtype_code(q), T, D, p, max_pos, _index(pos, T, "pos"), rot,
-                        1 if interleaved else 0, 1 if inverse else 0, _stream(stream))
-    return _check("lcp_rope", code)
+    return _check("lcp_rope", _serve.rope(q, q_out, table, pos, k, k_out, interleaved, inverse, stream))
 
 
 def make_kv_cache(k, v, k_scale=None, v_scale=None):
     """lcp_kv_cache over pages [pages, heads, page_size, D] (bfloat16, float8_e4m3fn or int8) and, for the 8-bit
     formats, scales [pages, heads, page_size]."""
-    dtype, shape = k.dtype, k.shape
-    fmt = _KV_FORMATS.get(dtype)
-    if fmt is None:
-        raise TypeError("unsupported cache dtype %s" % dtype)
-    if len(shape) != 4 or shape != v.shape or dtype is not v.dtype or not (k.is_contiguous() and v.is_contiguous()):
-        raise ValueError("k and v must be contiguous [pages, heads, page_size, D] of one dtype")
-    sk = sv = None
-    if fmt != LCP_KV_BF16:
-        if k_scale is None or v_scale is None:
-            raise ValueError("8-bit caches need k_scale and v_scale")
-        for s in (k_scale, v_scale):
-            if s.dtype is not _F32 or s.shape != shape[:3] or not s.is_contiguous():
-                raise ValueError("scales must be contiguous float32 [pages, heads, page_size]")
-        sk, sv = k_scale.data_ptr(), v_scale.data_ptr()
-    pages, heads, ps, D = shape
-    return lcp_kv_cache(k.data_ptr(), v.data_ptr(), sk, sv, fmt, pages, ps, heads, D)
+    return lcp_kv_cache.from_buffer_copy(_serve.cache(k, v, k_scale, v_scale))
 
 
 def lcp_kv_append(cache, k, v, slots, q=None, q_out=None, table=None, pos=None, interleaved=False, stream=None):
-    T, D = k.shape[0], cache.D
-    hk, hv = _heads(k, None, D, _BF16, "k"), _heads(v, None, D, _BF16, "v")
-    if v.shape[0] != T:
-        raise ValueError("k and v need one number of tokens")
-    hq = None
-    if q is not None:
-        if q.shape[0] != T or q_out is None or table is None:
-            raise ValueError("q needs k's number of tokens, an output and a table")
-        hq = _heads(q, q_out, D, _BF16, "q")
-    p = pp = None
-    max_pos = rot = 0
-    if table is not None:
-        p, max_pos, rot = _table(table)
-        pp = _index(pos, T, "pos")
-    code = LIB.lcp_kv_append(ctypes.byref(cache), hq, hk, hv, T, _index(slots, T, "slots"),
-                             p, max_pos, pp, rot, 1 if interleaved else 0, _stream(stream))
-    return _check("lcp_kv_append", code)
+    return _check("lcp_kv_append", _serve.append(cache, k, v, slots, q, q_out, table, pos, interleaved,
+                                                 stream))
 
 
 def lcp_kv_read(cache, slots, k_out, v_out, stream=None):
-    T = slots.shape[0]
-    shape = (T, cache.heads, cache.D)
-    if k_out.shape != shape or v_out.shape != shape or v_out.dtype is not k_out.dtype or not (
-            k_out.is_contiguous() and v_out.is_contiguous()):
-        raise ValueError("k_out and v_out must be contiguous [T, heads, D] of one dtype")
-    code = LIB.lcp_kv_read(ctypes.byref(cache), _index(slots, T, "slots"), T, k_out.data_ptr(), v_out.data_ptr(),
-                           dtype_code(k_out), _stream(stream))
-    return _check("lcp_kv_read", code)
+    return _check("lcp_kv_read", _serve.read(cache, slots, k_out, v_out, stream)[0])
 
 
 def lcp_attn_decode_workspace_bytes(cache, B, hq, max_len, window=0):
@@ -493,20 +406,6 @@ def lcp_attn_decode_workspace_bytes(cache, B, hq, max_len, window=0):
 
 
 def lcp_attn_decode(cache, q, pages, lens, max_len, out, ws=None, lse=None, scale=None, window=0, stream=None):
-    """ws: a uint8 tensor of lcp_attn_decode_workspace_bytes bytes, or None where that says 0."""
-    shape = q.shape
-    B, hq, D = shape
-    row, head, one = q.stride()
-    if q.dtype is not _BF16 or D != cache.D or one != 1 or (hq > 1 and head != D):
-        raise ValueError("q must be [B, heads, %d] bfloat16 with adjacent heads" % cache.D)
-    if out.shape != shape or not out.is_contiguous():
-        raise ValueError("out must be contiguous and have q's shape")
-    if lse is not None and (lse.shape != (B, hq) or lse.dtype is not _F32 or not lse.is_contiguous()):
-        raise ValueError("lse must be contiguous float32 [B, heads]")
-    if pages.dim() != 2 or pages.shape[0] != B or pages.dtype is not _I32 or not pages.is_contiguous():
-        raise ValueError("pages must be contiguous int32 [B, max_pages]")
-    code = LIB.lcp_attn_decode(ctypes.byref(cache), q.data_ptr(), row if B > 1 else hq * D, B, hq, pages.data_ptr(),
-                               pages.shape[1], _index(lens, B, "lens"), max_len, D ** -0.5 if scale is None else scale,
-                               window, out.data_ptr(), dtype_code(out), None if lse is None else lse.data_ptr(),
-                               None if ws is None else ws.data_ptr(), 0 if ws is None else ws.nbytes, _stream(stream))
-    return _check("lcp_attn_decode", code)
+    """ws: a tensor of lcp_attn_decode_workspace_bytes bytes, or None where that says 0."""
+    return _check("lcp_attn_decode", _serve.attend(cache, q, pages, lens, max_len, out, lse, ws, scale, window, False,
+                                                   stream)[0])

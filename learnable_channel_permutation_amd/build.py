@@ -1,22 +1,26 @@
-"""Build liblcp.so (gfx950) in-tree from csrc/*.hip with hipcc.
+"""Build liblcp.so (gfx950) in-tree from csrc/*.hip with hipcc, and _serve.so,
+the marshalling of the serving calls, from csrc/bind.cpp with g++.
 
     python learnable_channel_permutation_amd/build.py
 
-Objects go to <repo>/_build/, the shared library next to this file. Every
+Objects go to <repo>/_build/, the shared libraries next to this file. Every
 invocation recompiles every source.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "liblcp.so")
+BIND = os.path.join(PKG, "_serve.so")
 ARCH = "gfx950"
 
 # -packed-fp32-ops: keep fp32 arithmetic in plain (unpacked) VALU instructions.
@@ -51,20 +55,47 @@ def _compile(src):
     return obj
 
 
+def _compile_bind():
+    """csrc/bind.cpp against the headers of Python and torch (torch itself is not imported)."""
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    obj = os.path.join(OBJ, "host", "bind.o")        # apart from the library's objects
+    os.makedirs(os.path.dirname(obj), exist_ok=True)
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-isystem", os.path.join(torch, "include"), "-isystem",
+           os.path.join(torch, "include", "torch", "csrc", "api", "include"), "-isystem",
+           sysconfig.get_paths()["include"], "-c", os.path.join(CSRC, "bind.cpp"), "-o", obj]
+    p = subprocess.run(cmd, capture_output=True, text=True)
+    if p.returncode != 0:
+        raise RuntimeError("g++ failed for bind.cpp:\n%s" % p.stderr)
+    return obj, os.path.join(torch, "lib")
+
+
+def _link_bind(obj, torch_lib):
+    tmp = BIND + ".tmp"
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", PKG, "-llcp", "-L", torch_lib, "-lc10", "-ltorch_cpu", "-ltorch",
+           "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+    p = subprocess.run(cmd, capture_output=True, text=True)
+    if p.returncode != 0:
+        raise RuntimeError("link of _serve.so failed:\n%s" % p.stderr)
+    os.replace(tmp, BIND)
+
+
 def build(verbose=False):
     os.makedirs(OBJ, exist_ok=True)
     srcs = sources()
-    workers = min(len(srcs), int(os.environ.get("MAX_JOBS", "8")))
+    workers = min(len(srcs) + 1, int(os.environ.get("MAX_JOBS", "8")))
     with cf.ThreadPoolExecutor(max_workers=workers) as ex:
+        bind = ex.submit(_compile_bind)
         objs = list(ex.map(_compile, srcs))
+        bind = bind.result()
     tmp = LIB + ".tmp"
     cmd = [_hipcc(), "--offload-arch=" + ARCH, "-shared", "-fPIC", "-o", tmp] + objs
     p = subprocess.run(cmd, capture_output=True, text=True)
     if p.returncode != 0:
         raise RuntimeError("link failed:\n%s" % p.stderr)
     os.replace(tmp, LIB)
+    _link_bind(*bind)
     if verbose:
-        print("built", LIB)
+        print("built", LIB, "and", BIND)
     return LIB
 
 

@@ -133,6 +133,7 @@ def test_attend_refusals():
 def test_python_forms_check_shapes_and_types():
     """Wrong dtypes, shapes and layouts are errors in Python, not reads of something else."""
     import learnable_channel_permutation_amd as lcp
+    OTHER = "^(?!tensors must be on the GPU)"        # the device is looked at last
     bf = torch.bfloat16
     x, t = torch.zeros(3, 2, 64, dtype=bf), torch.zeros(9, 32, 2)
     pos = torch.zeros(3, dtype=torch.int32)
@@ -140,7 +141,7 @@ def test_python_forms_check_shapes_and_types():
                dict(q=x.transpose(1, 2)), dict(q_out=x[:2]), dict(q_out=x.float()), dict(k=x),
                dict(k=x[:2], k_out=x[:2]), dict(k=x.float(), k_out=x.float())):
         a = {**dict(q=x, q_out=torch.empty_like(x), table=t, pos=pos), **kw}
-        with pytest.raises(ValueError):
+        with pytest.raises(ValueError, match=OTHER):
             lcp.lcp_rope(**a)
     with pytest.raises(TypeError):
         h = x.half()
@@ -150,22 +151,28 @@ def test_python_forms_check_shapes_and_types():
     with pytest.raises(TypeError):
         lcp.PagedKVCache(k.half(), k.half())
     for a in ((k, k, None, s), (k, k, s, s.double()), (k, k[:2], s, s), (k.transpose(1, 2), k.transpose(1, 2), s, s)):
-        with pytest.raises(ValueError):
+        with pytest.raises(ValueError, match=OTHER):
             lcp.PagedKVCache(*a)
     c = lcp.PagedKVCache(k, k.clone(), s, s.clone())
-    with pytest.raises(ValueError):
+    with pytest.raises(ValueError, match=OTHER):
         c.append(x, x[:2], pos)
-    with pytest.raises(ValueError):
+    with pytest.raises(ValueError, match=OTHER):
         c.append(x, x, pos.long())
-    with pytest.raises(ValueError):
+    with pytest.raises(ValueError, match=OTHER):
         c.append(x, x, pos, q=x)
-    with pytest.raises(ValueError):
+    with pytest.raises(ValueError, match=OTHER):
         c.read(pos, torch.empty(3, 2, 65), torch.empty(3, 2, 65))
     pt, ln = torch.zeros(3, 2, dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
     for a, kw in (((x.float(), pt, ln), {}), ((x, pt[:2], ln), {}), ((x, pt, ln.long()), {}),
                   ((x, pt, ln), dict(out=torch.empty(3, 2, 32))), ((x, pt, ln), dict(lse=torch.empty(3, 2).double())),
                   ((torch.zeros(3, 64, 2, dtype=bf).transpose(1, 2), pt, ln), {})):
-        with pytest.raises(ValueError):
+        with pytest.raises(ValueError, match=OTHER):
             c.attend(*a, **kw)
     with pytest.raises(lcp.LcpError):       # heads of q not a multiple of the cache's
         c.attend(torch.zeros(3, 3, 64, dtype=bf), pt, ln)
+    for call in (lambda: lcp.lcp_rope(x, torch.empty_like(x), t, pos), lambda: c.append(x, x, pos),
+                 lambda: c.read(pos), lambda: c.attend(x, pt, ln)):
+        with pytest.raises(ValueError, match="on the GPU"):
+            call()
+    with pytest.raises(ValueError, match=OTHER):
+        lcp.lcp_rope(x, None, t, pos)
