@@ -83,8 +83,10 @@ struct Plan {
   int2* cuts;            // [B][units] place of the first piece, number of pieces
 };
 // Direct against dealt with its second kernel, us a pass: K of 128 KB (1 x 1000
-// fp8) 12.7 / 17.0, 192 KB (1 x 1500; 64 x 1500) 13.8 / 16.9; 27.9 / 31.6,
-// 256 KB (1 x 2000; 8 x 1000 bf16) 18.1 / 17.0; 17.4 / 16.8.
+// fp8; 64 x 1000) 9.9 / 11.9; 19.9 / 24.8, 192 KB (x 1500) 12.9 / 11.7; 27.4 /
+// 30.5, 256 KB (x 2000) 16.0 / 11.8; 34.9 / 36.0. One compute unit takes in about
+// 50 KB a us, so that a direct workgroup of eight waves instead of four was slower
+// (1 x 1000: 10.9 us).
 constexpr int kDirect = 192 << 10;
 // Cost of beginning and ending a unit, in steps: 2, 4, 8, 12 gave 53.1, 46.9, 46.4,
 // 47.7 us at 48 x 4096 fp8 and 56.5, 51.4, 50.0, 51.4 at 96 x 2048.
