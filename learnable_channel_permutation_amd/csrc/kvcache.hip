@@ -139,7 +139,7 @@ __device__ __forceinline__ uint2 encode8(const float* f, float s, float inv) {
 // rotated, quantised and written in one pass. The bytes bound it: a row is read
 // once and its codes written once. 16001 tokens x (32 + 32 + 32) heads of 128,
 // fp8 (655 MB), with the read back of 20097 slots (494 MB): one wave a row and one
-// thread an element 1320 us, these two kernels 208 us = 5.6 TB/s.
+// thread an element 1320 us, these two kernels 207 us = 5.6 TB/s.
 template <int FMT, int D, bool STREAM>
 __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendArgs a, int64_t n) {
   typedef RopeChunk<uint16_t, 8> C;
