@@ -22,8 +22,9 @@
 //     transposition is a byte permutation within the lane.
 // 8-bit codes become bf16 exactly; their scales multiply the scores and the
 // weights. Groups of fewer than 16 heads leave columns of the products empty,
-// which costs nothing while the bytes bound it; groups of more read K and V once
-// for every 16 heads, from the L2 when the workgroups meet there.
+// which costs nothing while the bytes bound it. In larger groups two tiles of 16
+// heads share a wave's loads; beyond that K and V are read again, from the L2 when
+// the workgroups meet there.
 //
 // Measured (us; bytes of K, V and scales over time), 64 heads in 8 groups of 128
 // channels unless said: 128 sequences up to 8192, bf16, 2.15 GB 340 (6.3 TB/s);
@@ -60,8 +61,9 @@ __device__ __forceinline__ uint32_t codes2(uint32_t w) {
   return pack2_exact((float)c0, (float)c1);
 }
 
-// How the work is dealt. A unit is one sequence, one key/value head and up to 16
-// of its query heads; its work is counted in steps.
+// How the work is dealt. A unit is one sequence, one key/value head and up to
+// 16 HT of its query heads (HT tiles of 16, which share the loads of K and V); its
+// work is counted in steps.
 //   direct (wgs == 0): a workgroup a unit, no second kernel. Where no unit can
 //     have more than kDirect bytes of K.
 //   else: the steps of all units in a row, each unit led by kExtra steps that
@@ -74,9 +76,9 @@ __device__ __forceinline__ uint32_t codes2(uint32_t w) {
 //     pieces of each unit in order.
 struct Plan {
   int wgs;
-  int G, ht;             // query heads of a group, head tiles of 16 in it
-  int units;             // units of a sequence: heads * ht
-  int nh;                // query heads of a unit (the last tile may have fewer)
+  int G, tile, gu;       // query heads of a group, of a unit at most (16 HT), and units of a group
+  int units;             // units of a sequence: heads * gu
+  int nh;                // query heads of a unit (a group's last one may have fewer)
   uint32_t tpm;          // ceil(2^32 / (page_size / 16)): page of a 16-token tile by a high product
   float* part;           // [2 wgs][nh][D]
   float2* ml;            // [2 wgs][nh] maximum and sum
@@ -183,10 +185,10 @@ __device__ __forceinline__ T once(const void* p) { return __builtin_nontemporal_
 
 // Waves per SIMD that the registers leave (checked by the compiler): what
 // hides the loads' latency, and the number of workgroups that run at a time.
-constexpr int waves_for(int D) { return D == 64 ? 4 : D == 128 ? 3 : 2; }
+constexpr int waves_for(int D, int HT) { return (D == 64 ? 4 : D == 128 ? 3 : 2) - (HT - 1); }
 
-template <int FMT, int D, bool DEALT>
-__global__ __launch_bounds__(256, waves_for(D)) void attn_units_kernel(AttnArgs a, Plan p) {
+template <int FMT, int D, int HT, bool DEALT>
+__global__ __launch_bounds__(256, waves_for(D, HT)) void attn_units_kernel(AttnArgs a, Plan p) {
   constexpr int E = FMT == KV_BF16 ? 2 : 1;
   constexpr int KL = D * E / 64;               // 16-byte K loads of a lane for 16 tokens
   constexpr int VC = D / 16;                   // channels of V a lane holds of each of its 8 tokens
@@ -199,8 +201,8 @@ __global__ __launch_bounds__(256, waves_for(D)) void attn_units_kernel(AttnArgs 
   // sums leave no room for them) in LDS, a quarter written by each wave
   constexpr bool QL = D == 256 && E == 2;
   constexpr int QR = QL ? QF / kWaves : QF;    // fragments that a wave loads
-  __shared__ float so[kWaves][16][OS];
-  __shared__ float sm[kWaves][16], sl[kWaves][16];
+  __shared__ float so[kWaves][16 * HT][OS];
+  __shared__ float sm[kWaves][16 * HT], sl[kWaves][16 * HT];
   __shared__ u32x4 sq[QL ? QF : 1][QL ? 64 : 1];
   __shared__ uint32_t scan[kWaves + 2];
 
@@ -253,7 +255,7 @@ __global__ __launch_bounds__(256, waves_for(D)) void attn_units_kernel(AttnArgs 
   int lo, end, t, hk, nh, head0, last;
   bool whole;
   const int* pages;
-  u32x4 qf[QR];
+  u32x4 qf[HT][QR];
   const int tp = a.c.ps >> 4;
   // the page of the 16 tokens from t on (past the end: of the last ones), its
   // number, and the cache row; row 0 stands in where there is nothing to read
@@ -327,9 +329,9 @@ __global__ __launch_bounds__(256, waves_for(D)) void attn_units_kernel(AttnArgs 
       left = 0;
     }
     whole = r0 == 0 && r1 == sp.steps;
-    hk = u / p.ht;
-    const int h0 = u % p.ht * 16;
-    nh = min(16, p.G - h0);
+    hk = u / p.gu;
+    const int h0 = u % p.gu * (16 * HT);
+    nh = min(16 * HT, p.G - h0);
     head0 = hk * p.G + h0;
     lo = sp.lo;
     const int begin = lo & ~(kStep - 1);
@@ -337,14 +339,16 @@ __global__ __launch_bounds__(256, waves_for(D)) void attn_units_kernel(AttnArgs 
     last = max(end - 1, 0) >> 4;
     t = begin + r0 * kStep + wave * kStep;
     pages = a.pages + (int64_t)b * a.max_pages;
-    // Q fragments: head c16, the channels that the K loads bring
+    // Q fragments: head c16 of each tile, the channels that the K loads bring
 #pragma unroll
-    for (int m = 0; m < QR; ++m) {
-      const int f = QL ? QR * wave + m : m;
-      const int d = E == 2 ? 32 * f + 8 * g : 64 * (f >> 1) + 16 * g + 8 * (f & 1);
-      qf[m] = u32x4{0, 0, 0, 0};
-      if (c16 < nh) qf[m] = *(const u32x4*)(a.q + b * a.qrow + (int64_t)(head0 + c16) * D + d);
-    }
+    for (int h = 0; h < HT; ++h)
+#pragma unroll
+      for (int m = 0; m < QR; ++m) {
+        const int f = QL ? QR * wave + m : m;
+        const int d = E == 2 ? 32 * f + 8 * g : 64 * (f >> 1) + 16 * g + 8 * (f & 1);
+        qf[h][m] = u32x4{0, 0, 0, 0};
+        if (16 * h + c16 < nh) qf[h][m] = *(const u32x4*)(a.q + b * a.qrow + (int64_t)(head0 + 16 * h + c16) * D + d);
+      }
     cur[0] = half_at(t, uniform(pages, page_at(t)));
     cur[1] = half_at(t + 16, uniform(pages, page_at(t + 16)));
     id0 = uniform(pages, page_at(t + kRound));
@@ -364,8 +368,8 @@ __global__ __launch_bounds__(256, waves_for(D)) void attn_units_kernel(AttnArgs 
     return true;
   };
 
-  f32x4 o[VC];
-  float m = kLowest, l = 0.f;
+  f32x4 o[HT][VC];
+  float m[HT], l[HT];
   bool done = false;                           // whether o, m and l hold a finished unit: the last one
   int nh_ = 0, place_ = 0;
   bool whole_ = false;
@@ -376,15 +380,19 @@ __global__ __launch_bounds__(256, waves_for(D)) void attn_units_kernel(AttnArgs 
     if (done) {
       // join the waves: O^T tile j, register i of lane (h, g) is channel
       // 16 VP (j / VP) + VP (4 g + i) + j % VP of head h
-      l = xor32_sum(xor16_sum(l));
-      if (g == 0) { sm[wave][c16] = m; sl[wave][c16] = l; }
-      if (c16 < nh_) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+      for (int t = 0; t < HT; ++t) {
+        const int h = 16 * t + c16;
+        l[t] = xor32_sum(xor16_sum(l[t]));
+        if (g == 0) { sm[wave][h] = m[t]; sl[wave][h] = l[t]; }
+        if (h < nh_) {
 #pragma unroll
-          for (int j = 0; j < VC; j += 4)
-            *(f32x4*)&so[wave][c16][16 * VP * (j / VP) + VP * (4 * g + i) + j % VP] =
-                f32x4{o[j][i], o[j + 1][i], o[j + 2][i], o[j + 3][i]};
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < VC; j += 4)
+              *(f32x4*)&so[wave][h][16 * VP * (j / VP) + VP * (4 * g + i) + j % VP] =
+                  f32x4{o[t][j][i], o[t][j + 1][i], o[t][j + 2][i], o[t][j + 3][i]};
+        }
       }
       __syncthreads();
       for (int idx = threadIdx.x; idx < nh_ * (D / 4); idx += 256) {
@@ -414,23 +422,27 @@ __global__ __launch_bounds__(256, waves_for(D)) void attn_units_kernel(AttnArgs 
     if (!more) return;
     if (QL) {
 #pragma unroll
-      for (int m = 0; m < QR; ++m) sq[QR * wave + m][lane] = qf[m];
+      for (int f = 0; f < QR; ++f) sq[QR * wave + f][lane] = qf[0][f];       // HT is 1
       __syncthreads();
     }
 #pragma unroll
-    for (int j = 0; j < VC; ++j) o[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    m = kLowest;
-    l = 0.f;
+    for (int h = 0; h < HT; ++h) {
+#pragma unroll
+      for (int j = 0; j < VC; ++j) o[h][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      m[h] = kLowest;
+      l[h] = 0.f;
+    }
     for (; t < end; t += kRound) {
       nxt[0] = half_at(t + kRound, id0);
       nxt[1] = half_at(t + kRound + 16, id1);
       id0 = uniform(pages, page_at(t + 2 * kRound));
       id1 = uniform(pages, page_at(t + 2 * kRound + 16));
-      // scores of tokens 16 i + 4 g + e for head c16
-      f32x4 s[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      // scores of tokens 16 i + 4 g + e for head c16 of each tile
+      f32x4 s[HT][2];
+#pragma unroll
+      for (int h = 0; h < HT; ++h) s[h][0] = s[h][1] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int mm = 0; mm < QF; ++mm) {
-        const u32x4 q = QL ? sq[QL ? mm : 0][QL ? lane : 0] : qf[QL ? 0 : mm];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           u32x4 kk;
@@ -440,14 +452,18 @@ __global__ __launch_bounds__(256, waves_for(D)) void attn_units_kernel(AttnArgs 
             const uint32_t w0 = kf[i][mm >> 1][2 * (mm & 1)], w1 = kf[i][mm >> 1][2 * (mm & 1) + 1];
             kk = u32x4{codes2<FMT, false>(w0), codes2<FMT, true>(w0), codes2<FMT, false>(w1), codes2<FMT, true>(w1)};
           }
-          s[i] = mfma16(kk, q, s[i]);
+#pragma unroll
+          for (int h = 0; h < HT; ++h)
+            s[h][i] = mfma16(kk, QL ? sq[QL ? mm : 0][QL ? lane : 0] : qf[h][QL ? 0 : mm], s[h][i]);
         }
       }
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (E == 1) s[i] *= ks[i] * a.scale2;
-        else s[i] *= a.scale2;
-      }
+      for (int h = 0; h < HT; ++h)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (E == 1) s[h][i] *= ks[i] * a.scale2;
+          else s[h][i] *= a.scale2;
+        }
       const bool full = cur[0].ok && cur[1].ok && t >= lo && t + kStep <= end;
       if (!full) {
         // what lies outside the counted tokens has no effect whatever its bits:
@@ -458,7 +474,8 @@ __global__ __launch_bounds__(256, waves_for(D)) void attn_units_kernel(AttnArgs 
           for (int e = 0; e < 4; ++e) {
             const int tt = t + 16 * i + 4 * g + e;
             const bool in = cur[i].ok && tt >= lo && tt < end;
-            s[i][e] = in ? s[i][e] : -__builtin_inff();
+#pragma unroll
+            for (int h = 0; h < HT; ++h) s[h][i][e] = in ? s[h][i][e] : -__builtin_inff();
             if (E == 1) vs[i][e] = in ? vs[i][e] : 0.f;
 #pragma unroll
             for (int w = 0; w < VW; ++w) vw[4 * i + e][w] = in ? vw[4 * i + e][w] : 0u;
@@ -469,30 +486,33 @@ __global__ __launch_bounds__(256, waves_for(D)) void attn_units_kernel(AttnArgs 
       // so that the waits can count on the loads in between
       load_k(nxt);
       __builtin_amdgcn_sched_barrier(0);
-      float top = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
-                        fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
-      if (__any(top > m + kLazy)) {
-        top = xor32_max(xor16_max(top));         // the head's four lanes agree on the maximum
-        const float mn = fmaxf(m, top), r = exp2_(m - mn);
-        m = mn;
-        l *= r;
-#pragma unroll
-        for (int j = 0; j < VC; ++j) o[j] *= r;
-      }
       // p in two bfloat16 parts (their sum is p to 2^-16): the weights reach the
       // sums with what fp32 arithmetic on them would keep
-      u32x4 ph, pl;
+      u32x4 ph[HT], pl[HT];
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int h = 0; h < HT; ++h) {
+        float top = fmaxf(fmaxf(fmaxf(s[h][0][0], s[h][0][1]), fmaxf(s[h][0][2], s[h][0][3])),
+                          fmaxf(fmaxf(s[h][1][0], s[h][1][1]), fmaxf(s[h][1][2], s[h][1][3])));
+        if (__any(top > m[h] + kLazy)) {
+          top = xor32_max(xor16_max(top));       // the head's four lanes agree on the maximum
+          const float mn = fmaxf(m[h], top), r = exp2_(m[h] - mn);
+          m[h] = mn;
+          l[h] *= r;
 #pragma unroll
-        for (int e = 0; e < 4; e += 2) {
-          float p0 = exp2_(s[i][e] - m), p1 = exp2_(s[i][e + 1] - m);
-          l += p0 + p1;
-          if (E == 1) { p0 *= vs[i][e]; p1 *= vs[i][e + 1]; }
-          const uint32_t hi = pack2(p0, p1);
-          ph[2 * i + e / 2] = hi;
-          pl[2 * i + e / 2] = pack2(p0 - lo_bf(hi), p1 - hi_bf(hi));
+          for (int j = 0; j < VC; ++j) o[h][j] *= r;
         }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; e += 2) {
+            float p0 = exp2_(s[h][i][e] - m[h]), p1 = exp2_(s[h][i][e + 1] - m[h]);
+            l[h] += p0 + p1;
+            if (E == 1) { p0 *= vs[i][e]; p1 *= vs[i][e + 1]; }
+            const uint32_t hi = pack2(p0, p1);
+            ph[h][2 * i + e / 2] = hi;
+            pl[h][2 * i + e / 2] = pack2(p0 - lo_bf(hi), p1 - hi_bf(hi));
+          }
+      }
 #pragma unroll
       for (int j = 0; j < VC; ++j) {
         u32x4 vv;
@@ -509,8 +529,11 @@ __global__ __launch_bounds__(256, waves_for(D)) void attn_units_kernel(AttnArgs 
             vv[w] = j & 1 ? codes2<FMT, true>(pr) : codes2<FMT, false>(pr);
           }
         }
-        o[j] = mfma16(vv, ph, o[j]);
-        o[j] = mfma16(vv, pl, o[j]);
+#pragma unroll
+        for (int h = 0; h < HT; ++h) {
+          o[h][j] = mfma16(vv, ph[h], o[h][j]);
+          o[h][j] = mfma16(vv, pl[h], o[h][j]);
+        }
       }
       __builtin_amdgcn_sched_barrier(0);
       load_v(nxt);
@@ -556,7 +579,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, Plan p, int 
     const int place0 = uniform((const int*)p.cuts, 2 * unit);
     const int pieces = some ? uniform((const int*)p.cuts, 2 * unit + 1) : 0;
     if (pieces == 1) continue;                 // written whole by its workgroup
-    const int h0 = u % p.ht * 16, nh = min(16, p.G - h0);
+    const int h0 = u % p.gu * p.tile, nh = min(p.tile, p.G - h0);
     for (int h = ROWS ? group % p.nh : tg; h < nh; h += ROWS ? nh : TG) {
       float M = kLowest, L = 0.f;
       f32x4 y = {0.f, 0.f, 0.f, 0.f};
@@ -585,7 +608,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, Plan p, int 
         if (tg != 0) return;
         for (int w = 1; w < TG; ++w) add(M, L, y, sm[w], sl[w], so[w][td]);
       }
-      put_row<D>(a, (int64_t)b * a.hq + u / p.ht * p.G + h0 + h, td, y, M, L);
+      put_row<D>(a, (int64_t)b * a.hq + u / p.gu * p.G + h0 + h, td, y, M, L);
     }
   }
 }
@@ -595,26 +618,50 @@ inline size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 Plan make_plan(const KvCache& c, int B, int hq, int max_len, int window) {
   Plan p{};
   p.G = hq / c.heads;
-  p.ht = (p.G + 15) / 16;
-  p.units = c.heads * p.ht;
-  p.nh = p.G < 16 ? p.G : 16;
   const int tp = c.ps / 16;
   p.tpm = tp == 1 ? 0u : (uint32_t)(((1ull << 32) + tp - 1) / tp);
   // the tokens a sequence can span: a window begins anywhere in a step
   int64_t span = max_len;
   if (window && window + (int64_t)kStep - 1 < span) span = window + (int64_t)kStep - 1;
-  if (span * c.D * (c.format == KV_BF16 ? 2 : 1) > kDirect) p.wgs = 256 * waves_for(c.D);
+  const bool dealt = span * c.D * (c.format == KV_BF16 ? 2 : 1) > kDirect;
+  // Two head tiles a unit where a group has them, the registers hold them and the
+  // work is enough: below it the halved number of units costs more than the bytes.
+  // One tile against two, us (32 heads a group, 2 groups): dealt, 4 / 8 / 32 x 4000
+  // 13.5 / 14.8, 21.9 / 16.9, 52.1 / 35.5 (bf16, 128), 12.9 / 14.7, 16.7 / 15.9,
+  // 34.3 / 27.7 (fp8), 12.0 / 12.5, 14.7 / 13.2, 32.8 / 25.6 (bf16, 64); direct, 64 /
+  // 256 x 500 13.1 / 13.7, 54.1 / 26.9 (bf16, 128), 8.5 / 10.7, 30.2 / 18.9 (fp8).
+  // 64 x 8192 with one group of 32, 64 heads 84.8 / 55.1, 136 / 82.
+  const int64_t units1 = (int64_t)B * c.heads * ((p.G + 15) / 16);
+  const bool enough = dealt ? units1 * ((span + kStep - 1) / kStep) > 3 * 256 * waves_for(c.D, 1) : units1 > 256;
+  const int HT = p.G > 16 && c.D <= 128 && enough ? 2 : 1;
+  p.tile = 16 * HT;
+  p.gu = (p.G + p.tile - 1) / p.tile;
+  p.units = c.heads * p.gu;
+  p.nh = std::min(p.G, p.tile);
+  if (dealt) p.wgs = 256 * waves_for(c.D, HT);
   return p;
 }
 
-template <int FMT, int D>
+// The workspace's parts, of either number of tiles: a workspace for the largest
+// call serves the smaller ones.
+struct Space {
+  size_t part, ml, cuts;       // bytes
+};
+Space space_for(const KvCache& c, int B, const Plan& p) {
+  size_t rows = (size_t)256 * waves_for(c.D, 1) * std::min(p.G, 16);
+  if (c.D <= 128) rows = std::max(rows, (size_t)256 * waves_for(c.D, 2) * std::min(p.G, 32));
+  return {align256(2 * rows * c.D * 4), align256(2 * rows * 8),
+          align256((size_t)B * c.heads * ((p.G + 15) / 16) * 8)};
+}
+
+template <int FMT, int D, int HT>
 hipError_t run(const AttnArgs& a, const Plan& p, hipStream_t s) {
   const int64_t units = (int64_t)a.B * p.units;
   if (p.wgs == 0) {
-    attn_units_kernel<FMT, D, false><<<(unsigned)units, 256, 0, s>>>(a, p);
+    attn_units_kernel<FMT, D, HT, false><<<(unsigned)units, 256, 0, s>>>(a, p);
     return hipGetLastError();
   }
-  attn_units_kernel<FMT, D, true><<<(unsigned)p.wgs, 256, 0, s>>>(a, p);
+  attn_units_kernel<FMT, D, HT, true><<<(unsigned)p.wgs, 256, 0, s>>>(a, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (units * 8 <= p.wgs) {
@@ -629,25 +676,25 @@ hipError_t run(const AttnArgs& a, const Plan& p, hipStream_t s) {
 
 template <int FMT>
 hipError_t run_d(const AttnArgs& a, const Plan& p, hipStream_t s) {
-  if (a.c.D == 64) return run<FMT, 64>(a, p, s);
-  if (a.c.D == 128) return run<FMT, 128>(a, p, s);
-  return run<FMT, 256>(a, p, s);
+  if (a.c.D == 256) return run<FMT, 256, 1>(a, p, s);
+  if (p.tile == 16) return a.c.D == 64 ? run<FMT, 64, 1>(a, p, s) : run<FMT, 128, 1>(a, p, s);
+  return a.c.D == 64 ? run<FMT, 64, 2>(a, p, s) : run<FMT, 128, 2>(a, p, s);
 }
 
 }  // namespace
 
 size_t attn_workspace_bytes(const KvCache& c, int B, int hq, int max_len, int window) {
   const Plan p = make_plan(c, B, hq, max_len, window);
-  const size_t n = (size_t)2 * p.wgs * p.nh;
-  return p.wgs ? align256(n * c.D * 4) + align256(n * 8) + align256((size_t)B * p.units * 8) : 0;
+  const Space n = space_for(c, B, p);
+  return p.wgs ? n.part + n.ml + n.cuts : 0;
 }
 
 hipError_t launch_attn_decode(const AttnArgs& a, hipStream_t s) {
   Plan p = make_plan(a.c, a.B, a.hq, a.max_len, a.window);
+  const Space n = space_for(a.c, a.B, p);
   p.part = a.ws;
-  const size_t n = (size_t)2 * p.wgs * p.nh;
-  p.ml = (float2*)((char*)a.ws + align256(n * a.c.D * 4));
-  p.cuts = (int2*)((char*)p.ml + align256(n * 8));
+  p.ml = (float2*)((char*)a.ws + n.part);
+  p.cuts = (int2*)((char*)p.ml + n.ml);
   if (a.c.format == KV_BF16) return run_d<KV_BF16>(a, p, s);
   if (a.c.format == KV_E4M3) return run_d<KV_E4M3>(a, p, s);
   return run_d<KV_INT8>(a, p, s);

@@ -398,6 +398,18 @@ def test_attend_many_sequences(B, n, hq, hk, D):
     check_attend("int8", [int(x) for x in lens], hq, hk, D, 32)
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "int8"])
+@pytest.mark.parametrize("hq,hk,D", [(17, 1, 64), (80, 2, 64), (32, 1, 128), (47, 1, 128), (49, 1, 128)])
+def test_attend_groups_of_more_than_16_heads(fmt, hq, hk, D):
+    """Enough work that two tiles of 16 heads share a wave's loads: dealt (long sequences) and direct (many short ones)."""
+    say("attend large groups", fmt, hq, hk, D)
+    rng = np.random.default_rng(hq)
+    lens = [int(x) for x in rng.integers(0, 4000, 30)] + [0, 1, 31, 32, 33, 4000]
+    check_attend(fmt, lens, hq, hk, D, 48, window=3500)
+    lens = [int(x) for x in rng.integers(0, 70, 140)] + [0, 1, 127, 128, 129]
+    check_attend(fmt, lens, hq, hk, D, 16, holes={(142, 2), (0, 0)})
+
+
 def test_attend_empty_batch_rows_and_zero_max_len():
     say("attend empty")
     check_attend("fp8", [0, 0, 0], 8, 2, 128, 16)

@@ -176,3 +176,18 @@ def test_python_forms_check_shapes_and_types():
             call()
     with pytest.raises(ValueError, match=OTHER):
         lcp.lcp_rope(x, None, t, pos)
+
+
+def test_workspace_of_the_largest_call_serves_the_smaller():
+    """The query grows with the batch and the length, whatever way of working the sizes lead to."""
+    import torch
+    L = _lib()
+    for D in (64, 128, 256):
+        k, s = torch.empty(4, 2, 16, D, dtype=torch.int8), torch.empty(4, 2, 16)
+        c = L.make_kv_cache(k, k.clone(), s, s.clone())
+        for G in (1, 16, 17, 31, 32, 40):
+            sizes = [[L.lcp_attn_decode_workspace_bytes(c, B, 2 * G, n) for n in (1, 700, 3000, 20000, 200000)]
+                     for B in (1, 5, 40, 300)]
+            for row, below in zip(sizes, sizes[1:] + [sizes[-1]]):
+                assert row == sorted(row)
+                assert all(x <= y for x, y in zip(row, below))
