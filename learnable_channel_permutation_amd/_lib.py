@@ -91,6 +91,7 @@ class lcp_kv_cache(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
                 ("v_scale", ctypes.c_void_p), ("format", ctypes.c_int), ("pages", ctypes.c_int),
                 ("page_size", ctypes.c_int), ("heads", ctypes.c_int), ("D", ctypes.c_int)]
+    gpu = -2                # the device index of its tensors (-1: the CPU's), -2: not known
 
 
 class LcpError(RuntimeError):
@@ -376,6 +377,10 @@ def make_rope_cfg(rot_dim, base=10000.0, scaling="none", factor=1.0, orig_len=0.
 def lcp_rope_table(cfg, table, stream=None):
     if tuple(table.shape[1:]) != (cfg.rot_dim // 2, 2) or table.dtype != torch.float32 or not table.is_contiguous():
         raise ValueError("table must be contiguous float32 [max_pos, %d, 2]" % (cfg.rot_dim // 2))
+    if not table.is_cuda:
+        raise ValueError("tensors must be on the GPU")
+    if table.get_device() != _current_device():
+        raise ValueError("tensors must be on the current GPU")
     return _check("lcp_rope_table", LIB.lcp_rope_table(ctypes.byref(cfg), table.shape[0], _p(table), _stream(stream)))
 
 
@@ -386,7 +391,9 @@ def lcp_rope(q, q_out, table, pos, k=None, k_out=None, interleaved=False, invers
 def make_kv_cache(k, v, k_scale=None, v_scale=None):
     """lcp_kv_cache over pages [pages, heads, page_size, D] (bfloat16, float8_e4m3fn or int8) and, for the 8-bit
     formats, scales [pages, heads, page_size]."""
-    return lcp_kv_cache.from_buffer_copy(_serve.cache(k, v, k_scale, v_scale))
+    c = lcp_kv_cache.from_buffer_copy(_serve.cache(k, v, k_scale, v_scale))
+    c.gpu = k.get_device()
+    return c
 
 
 def lcp_kv_append(cache, k, v, slots, q=None, q_out=None, table=None, pos=None, interleaved=False, stream=None):

@@ -1,14 +1,16 @@
 // Marshalling of the serving calls: torch tensors -> the C ABI of include/lcp.h.
 // A decode step makes several calls of a few microseconds of GPU time; reading
 // tensors through Python attributes and ctypes took longer than the kernels
-// (us a call on the host, before -> here: lcp_rope 7.6 -> 3.9, append 8.1 -> 4.1,
-// attend with its outputs 10.2 -> 6.0). Shapes, types and layouts are checked
-// here and raise ValueError or TypeError; everything else is the library's own
+// (us a call on the host, before -> here: lcp_rope 7.6 -> 3.8, append 8.1 -> 4.1,
+// attend with its outputs 10.2 -> 5.6). Shapes, types, layouts and devices are
+// checked here and raise ValueError or TypeError; everything else is the library's own
 // validation, whose status is returned.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/Stream.h>
+#include <c10/core/impl/VirtualGuardImpl.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -32,9 +34,17 @@ const at::Tensor& tensor(PyObject* o, const char* what) {
 // Optional arguments: None is a null pointer.
 const at::Tensor* maybe(PyObject* o, const char* what) { return o == Py_None ? nullptr : &tensor(o, what); }
 
-void on_gpu(std::initializer_list<const at::Tensor*> all) {
-  for (const at::Tensor* t : all)
-    if (t && !t->is_cuda()) throw Bad{"tensors must be on the GPU"};
+// The index of the GPU that all of a call's tensors (and its cache) are on.
+int on_gpu(std::initializer_list<const at::Tensor*> all, int cache = -2) {
+  int gpu = -2;
+  for (const at::Tensor* t : all) {
+    if (!t) continue;
+    if (!t->is_cuda() || cache == -1) throw Bad{"tensors must be on the GPU"};
+    const int at = t->get_device();
+    if ((gpu != -2 && at != gpu) || (cache >= 0 && at != cache)) throw Bad{"tensors must be on one GPU"};
+    gpu = at;
+  }
+  return gpu;
 }
 
 lcp_dtype dtype_of(const at::Tensor& t) { return t.scalar_type() == at::kFloat ? LCP_F32 : LCP_BF16; }
@@ -55,7 +65,12 @@ int small(PyObject* o) {
 // handle; called once the arguments are known to be good.
 PyObject* handle_of = nullptr;
 
-void* stream_of(PyObject* o) {
+// The stream's handle for tensors on a GPU, which has to be the current one.
+void* stream_of(PyObject* o, int gpu) {
+  const c10::impl::VirtualGuardImpl device(c10::DeviceType::CUDA);
+  const c10::Device now = device.getDevice();
+  if (now.index() != gpu) throw Bad{"tensors must be on the current GPU"};
+  if (o == Py_None && device.getStream(now).id() == 0) return nullptr;      // the default stream: no call into Python
   PyObject* h = handle_of ? PyObject_CallFunctionObjArgs(handle_of, o, nullptr) : nullptr;
   if (!h) throw Bad{handle_of ? nullptr : "use_streams has not been called"};
   void* s = PyLong_AsVoidPtr(h);
@@ -97,10 +112,18 @@ Table table_of(const at::Tensor& t) {
   return Table{static_cast<const float*>(t.data_ptr()), (int)t.size(0), (int)(2 * t.size(1))};
 }
 
-// The lcp_kv_cache in a bytes-like object.
+// The lcp_kv_cache in a bytes-like object, and the index of its GPU (-1: none, -2:
+// the object does not know).
 struct Cache {
   Py_buffer b{};
+  int gpu = -2;
   explicit Cache(PyObject* o) {
+    static PyObject* const name = PyUnicode_InternFromString("gpu");
+    if (PyObject* g = PyObject_GetAttr(o, name)) {
+      gpu = (int)PyLong_AsLong(g);
+      Py_DECREF(g);
+    }
+    PyErr_Clear();
     if (PyObject_GetBuffer(o, &b, PyBUF_SIMPLE) != 0) throw Bad{nullptr};
     if (b.len != (Py_ssize_t)sizeof(lcp_kv_cache)) {
       PyBuffer_Release(&b);
@@ -152,9 +175,9 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor &tab = tensor(a[2], "table must be a tensor"), &at_pos = tensor(a[3], "pos must be a tensor");
     const Table t = table_of(tab);
     const int32_t* pos = index_of(at_pos, T, "pos must be contiguous int32 [T]");
-    on_gpu({&q, &qo, k, ko, &tab, &at_pos});
+    const int gpu = on_gpu({&q, &qo, k, ko, &tab, &at_pos});
     const int inter = PyObject_IsTrue(a[6]), inverse = PyObject_IsTrue(a[7]);
-    void* s = stream_of(a[8]);
+    void* s = stream_of(a[8], gpu);
     int code;
     Py_BEGIN_ALLOW_THREADS
     code = lcp_rope(&hq, k ? &hk : nullptr, dtype_of(q), (int)T, (int)D, t.p, t.max_pos, pos, t.rot, inter, inverse, s);
@@ -181,6 +204,7 @@ PyObject* cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
       throw Bad{"k and v must be contiguous [pages, heads, page_size, D] of one dtype"};
     for (int i = 0; i < 4; ++i)
       if (k.size(i) > INT32_MAX) throw Bad{"the cache is too large"};
+    if (v.device() != k.device()) throw Bad{"the cache must be on one device"};
     c.k = k.data_ptr();
     c.v = v.data_ptr();
     c.pages = (int)k.size(0);
@@ -192,6 +216,7 @@ PyObject* cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
       for (const at::Tensor* t : s)
         if (!t || t->scalar_type() != at::kFloat || t->sizes() != k.sizes().slice(0, 3) || !t->is_contiguous())
           throw Bad{"8-bit caches need contiguous float32 scales [pages, heads, page_size]"};
+        else if (t->device() != k.device()) throw Bad{"the cache must be on one device"};
       c.k_scale = static_cast<float*>(s[0]->data_ptr());
       c.v_scale = static_cast<float*>(s[1]->data_ptr());
     }
@@ -223,9 +248,9 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     const at::Tensor& at_slots = tensor(a[3], "slots must be a tensor");
     const int32_t* slots = index_of(at_slots, T, "slots must be contiguous int32 [T]");
-    on_gpu({&k, &v, q, qo, tab, tab ? &THPVariable_Unpack(a[7]) : nullptr, &at_slots});
+    const int gpu = on_gpu({&k, &v, q, qo, tab, tab ? &THPVariable_Unpack(a[7]) : nullptr, &at_slots}, c.gpu);
     const int inter = PyObject_IsTrue(a[8]);
-    void* s = stream_of(a[9]);
+    void* s = stream_of(a[9], gpu);
     int code;
     Py_BEGIN_ALLOW_THREADS
     code = lcp_kv_append(c.get(), q ? &hq : nullptr, &hk, &hv, (int)T, slots, t.p, t.max_pos, pos, t.rot, inter, s);
@@ -254,10 +279,10 @@ PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (t && (t->sizes() != at::IntArrayRef(shape, 3) || t->scalar_type() != dt || !t->is_contiguous()))
         throw Bad{"k_out and v_out must be contiguous [T, heads, D] of one dtype"};
     const int32_t* index = index_of(slots, T, "slots must be contiguous int32 [T]");
-    on_gpu({&slots, given[0], given[1]});
+    const int gpu = on_gpu({&slots, given[0], given[1]}, c.gpu);
     for (int i = 0; i < 2; ++i)
       out[i] = given[i] ? *given[i] : at::empty(at::IntArrayRef(shape, 3), slots.options().dtype(dt));
-    void* s = stream_of(a[4]);
+    void* s = stream_of(a[4], gpu);
     int code;
     Py_BEGIN_ALLOW_THREADS
     code = lcp_kv_read(c.get(), index, (int)T, out[0].data_ptr(), out[1].data_ptr(), dtype_of(out[0]), s);
@@ -309,7 +334,7 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
     int code = lcp_attn_decode_workspace_bytes(c.get(), B, hq, max_len, window, &need);
     at::Tensor o, l, w;
     if (code == LCP_OK) {
-      on_gpu({&q, &pages, &lens, out, lse, ws});
+      const int gpu = on_gpu({&q, &pages, &lens, out, lse, ws}, c.gpu);
       if (out) o = *out;
       else o = at::empty(q.sizes(), q.options());
       if (lse) l = *lse;
@@ -317,7 +342,7 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (ws) w = *ws;
       else if (make && need) w = at::empty({(int64_t)need}, q.options().dtype(at::kByte));
       const int64_t row = B > 1 ? q.stride(0) : (int64_t)hq * D;
-      void* s = stream_of(a[11]);
+      void* s = stream_of(a[11], gpu);
       Py_BEGIN_ALLOW_THREADS
       code = lcp_attn_decode(c.get(), q.data_ptr(), row, B, hq, static_cast<const int32_t*>(pages.data_ptr()), P,
                              static_cast<const int32_t*>(lens.data_ptr()), max_len, (float)scale, window, o.data_ptr(),

@@ -262,6 +262,7 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvCache c, const int* slot
 template <int FMT, int D>
 hipError_t run_append(const KvAppendArgs& a, hipStream_t s) {
   const int64_t rows = (int64_t)a.T * (a.q.heads + 2 * a.c.heads), n = rows * (D / 16), grid = (n + 255) / 256;
+  if (n > kMaxThreads) return hipErrorInvalidConfiguration;
   const int64_t q = (int64_t)a.T * a.q.heads * D * 4, kv = (int64_t)a.T * a.c.heads * 2 * D * (FMT == KV_BF16 ? 4 : 3);
   if (q + kv > kStreamBytes) kv_append_kernel<FMT, D, true><<<(unsigned)grid, 256, 0, s>>>(a, n);
   else kv_append_kernel<FMT, D, false><<<(unsigned)grid, 256, 0, s>>>(a, n);
@@ -297,6 +298,7 @@ hipError_t launch_kv_append(const KvAppendArgs& a, hipStream_t s) {
   };
   if (!aligned(a.q) || !aligned(a.k) || !aligned(a.v)) {
     const int64_t rows = (int64_t)a.T * (a.q.heads + 2 * a.c.heads);
+    if (rows * 64 > kMaxThreads) return hipErrorInvalidConfiguration;
     kv_append_rows_kernel<<<(unsigned)rows, 64, 0, s>>>(a);
     return hipGetLastError();
   }

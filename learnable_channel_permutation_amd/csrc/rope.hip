@@ -125,6 +125,7 @@ __global__ __launch_bounds__(256) void rope_units_kernel(RopeArgs a, int64_t n) 
 template <typename E, int V>
 hipError_t run_units(const RopeArgs& a, hipStream_t s) {
   const int64_t rows = (int64_t)a.T * (a.q.heads + a.k.heads), n = rows * (a.D / (2 * V)), grid = (n + 255) / 256;
+  if (n > kMaxThreads) return hipErrorInvalidConfiguration;
   if (rows * a.D * 2 * (int64_t)sizeof(E) > kStreamBytes)
     rope_units_kernel<E, V, true><<<(unsigned)grid, 256, 0, s>>>(a, n);
   else
@@ -156,6 +157,7 @@ hipError_t launch_rope(const RopeArgs& a, int bf16, hipStream_t s) {
   if (!bf16 && fits(4, 4)) return run_units<float, 4>(a, s);
   const int64_t n = (int64_t)a.T * (a.q.heads + a.k.heads) * (a.rot / 2 + a.D - a.rot);
   const int64_t grid = (n + 255) / 256;
+  if (n > kMaxThreads) return hipErrorInvalidConfiguration;
   if (bf16) rope_pairs_kernel<uint16_t><<<(unsigned)grid, 256, 0, s>>>(a, n);
   else rope_pairs_kernel<float><<<(unsigned)grid, 256, 0, s>>>(a, n);
   return hipGetLastError();

@@ -64,6 +64,10 @@ __device__ __forceinline__ void store_as(void* p, T v) {
   else *(T*)p = v;
 }
 
+// A grid's threads are counted in 32 bits. A launcher whose call needs more returns
+// hipErrorInvalidConfiguration and launches nothing.
+constexpr int64_t kMaxThreads = ((int64_t)1 << 32) - 256;
+
 // Head rows [T][heads][D] with strides in elements, input and output.
 struct Rows {
   const void* x;

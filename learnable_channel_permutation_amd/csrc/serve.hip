@@ -56,12 +56,14 @@ int check_attn_sizes(const lcp_kv_cache* c, int B, int hq, int max_len, int wind
   // steps of 32 tokens over all sequences and head tiles in 32 bits
   const int64_t units = (int64_t)B * c->heads * ((hq / c->heads + 15) / 16);
   if (units * ((int64_t)max_len / 32 + 10) >= ((int64_t)1 << 31)) return LCP_E_INVAL;
+  if (units * 256 > kMaxThreads) return LCP_E_INVAL;           // a workgroup a unit
   return LCP_OK;
 }
 
-#define LCP_RUN(expr)                           \
-  do {                                          \
-    if ((expr) != hipSuccess) return LCP_E_HIP; \
+#define LCP_RUN(expr)                                                                             \
+  do {                                                                                            \
+    const hipError_t err = (expr);                                                                \
+    if (err != hipSuccess) return err == hipErrorInvalidConfiguration ? LCP_E_INVAL : LCP_E_HIP; \
   } while (0)
 
 }  // namespace
@@ -108,9 +110,8 @@ int lcp_rope(const lcp_heads* q, const lcp_heads* k, lcp_dtype dt, int T, int D,
     if (!good_rows_in(h) || !good_rows_out(h, T, D)) return LCP_E_INVAL;
     if (((uintptr_t)h->x & es) != 0 || ((uintptr_t)h->y & es) != 0) return LCP_E_INVAL;
   }
-  // rows and grids in 32 bits
   const int64_t rows = (int64_t)T * (q->heads + (k ? k->heads : 0));
-  if (rows >= ((int64_t)1 << 31) || rows * D >= ((int64_t)1 << 38)) return LCP_E_INVAL;
+  if (rows >= ((int64_t)1 << 31)) return LCP_E_INVAL;
   if (!aligned4(pos)) return LCP_E_INVAL;
   RopeArgs a{};
   a.q = rows_of(q);

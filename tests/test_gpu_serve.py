@@ -525,3 +525,16 @@ def test_example_decodes_through_the_deployed_layers():
                            "--batch", "3", "--train-steps", "2"])
         # bfloat16 output (2^-8) against fp32 on the same bfloat16 reads of fp8 codes, which are exact
         assert err < 2.0 ** -8 and torch.isfinite(y.float()).all() and y.shape == (3, 512)
+
+
+def test_tensors_on_the_cpu_are_refused():
+    """Also where only the cache is: its pointers would reach the kernels."""
+    say("cpu tensors")
+    host = lcp.PagedKVCache.empty(2, 16, 2, 64, device="cpu")
+    dev = lcp.PagedKVCache.empty(2, 16, 2, 64, device=DEV)
+    x = torch.zeros(1, 2, 64, dtype=torch.bfloat16, device=DEV)
+    i, p = torch.zeros(1, dtype=torch.int32, device=DEV), torch.zeros(1, 1, dtype=torch.int32, device=DEV)
+    for call in (lambda: host.append(x, x, i), lambda: host.read(i), lambda: host.attend(x, p, i),
+                 lambda: dev.append(x, x.cpu(), i), lambda: dev.read(i.cpu()), lambda: dev.attend(x, p, i.cpu())):
+        with pytest.raises(ValueError, match="on the GPU"):
+            call()

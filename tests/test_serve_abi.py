@@ -180,7 +180,6 @@ def test_python_forms_check_shapes_and_types():
 
 def test_workspace_of_the_largest_call_serves_the_smaller():
     """The query grows with the batch and the length, whatever way of working the sizes lead to."""
-    import torch
     L = _lib()
     for D in (64, 128, 256):
         k, s = torch.empty(4, 2, 16, D, dtype=torch.int8), torch.empty(4, 2, 16)
@@ -191,3 +190,34 @@ def test_workspace_of_the_largest_call_serves_the_smaller():
             for row, below in zip(sizes, sizes[1:] + [sizes[-1]]):
                 assert row == sorted(row)
                 assert all(x <= y for x, y in zip(row, below))
+
+
+def test_sizes_past_a_grid_are_refused():
+    """More threads than a grid counts: refused before the launch, in either form of the kernels."""
+    L = _lib()
+    big = _rows(L, heads=65536, xt=0, xh=0, yt=65536 * 128, yh=128)
+    odd = _rows(L, heads=65536, x=P + 2, xt=0, xh=0, yt=65536 * 128, yh=128)
+    for q, T in ((big, 1 << 14), (odd, 1 << 11)):
+        assert L.LIB.lcp_rope(ctypes.byref(q), None, L.LCP_BF16, T, 128, P, 10, P, 128, 0, 0, None) == L.LCP_E_INVAL
+        k = _rows(L, xt=0, xh=0)
+        assert L.LIB.lcp_kv_append(ctypes.byref(_cache(L)), ctypes.byref(q), ctypes.byref(k), ctypes.byref(k), T, P, P,
+                                   10, P, 128, 0, None) == L.LCP_E_INVAL
+    n = ctypes.c_size_t(0)
+    c = ctypes.byref(_cache(L, D=64, heads=1))
+    assert L.LIB.lcp_attn_decode_workspace_bytes(c, 1 << 24, 1, 16, 0, ctypes.byref(n)) == L.LCP_E_INVAL
+
+
+def test_cache_on_two_devices_is_refused():
+    L = _lib()
+    k, s = torch.zeros(4, 2, 16, 64, dtype=torch.int8), torch.zeros(4, 2, 16)
+    m = [torch.empty_like(k, device="meta"), torch.empty_like(s, device="meta")]
+    for a in ((k, m[0], s, s), (k, k.clone(), s, m[1])):
+        with pytest.raises(ValueError, match="one device"):
+            L.make_kv_cache(*a)
+    assert L.make_kv_cache(k, k.clone(), s, s.clone()).gpu == -1
+
+
+def test_table_on_the_cpu_is_refused():
+    L = _lib()
+    with pytest.raises(ValueError, match="on the GPU"):
+        L.lcp_rope_table(L.make_rope_cfg(64), torch.zeros(9, 32, 2))
