@@ -508,7 +508,8 @@ int lcp_kv_read(const lcp_kv_cache* c, const int32_t* slots, int T, void* k_out,
  * and t from max(0, n - window) (window 0: from 0) to n - 1,
  *   z_t = scale q.k_t,  m = max z,  l = sum exp(z_t - m),
  *   out = sum exp(z_t - m) v_t / l,  lse = m + ln l.
- * A sequence without tokens gives out 0 and lse -inf. What the cache holds in
+ * A sequence without tokens gives out 0 and lse -inf, and so does a row whose
+ * scores are all -inf. What the cache holds in
  * other slots (the rest of a last page, freed pages) has no effect, whatever
  * its bits; a NaN or an infinity among the counted tokens' values shows in the
  * rows that use it as NaN or infinity. The sums are fp32; the work is split over

@@ -32,7 +32,8 @@ __device__ __forceinline__ float row_scale(uint32_t a, int format) {
 }
 
 // Rows that are not 16-byte aligned: one wave per (token, head row), lane l
-// holds channels l, l + 64, .. and loads element by element.
+// holds channels l, l + 64, .. and loads element by element, which bounds it
+// (16001 tokens x 96 rows of 128: 660 us, aligned ones below 130).
 __global__ __launch_bounds__(64) void kv_append_rows_kernel(KvAppendArgs a) {
   const int lane = threadIdx.x, rows = a.q.heads + 2 * a.c.heads;
   const int64_t id = blockIdx.x;
@@ -208,7 +209,9 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendArgs a, int64_t 
   if (u == 0) (which == 1 ? a.c.ks : a.c.vs)[row] = sc;
 }
 
-// One thread per eight channels of a slot and head, K and V.
+// One thread per eight channels of a slot and head, K and V: one 16-byte store of
+// each (bf16), whole lines of both sides by adjacent lanes. The bytes bound it:
+// 16001 slots x 32 heads of 128, fp8 to bf16 (393 MB), 73 us = 5.4 TB/s.
 template <int FMT, bool BF, bool STREAM>
 __global__ __launch_bounds__(256) void kv_read_kernel(KvCache c, const int* slots, int64_t n, char* ko, char* vo) {
   const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;

@@ -6,6 +6,9 @@
 namespace lcp {
 namespace {
 
+// One thread an entry, in 64 bits: an angle of p theta radians has no accurate
+// fp32 form at large p. Written once and kept; the 64-bit functions bound it
+// (131072 positions x 64 pairs, 67 MB: 95 us).
 __global__ void rope_table_kernel(RopeFreq f, int n, float2* table) {
   const int64_t id = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   const int half = f.rot / 2;
@@ -34,7 +37,9 @@ __device__ __forceinline__ void store(float* p, int64_t i, float v) { p[i] = v; 
 __device__ __forceinline__ void store(uint16_t* p, int64_t i, float v) { p[i] = (uint16_t)f2bf(v); }
 
 // One thread per pair (or unrotated channel) of one head row; any size, stride
-// and alignment. In place: a thread reads its pair before it writes it.
+// and alignment. In place: a thread reads its pair before it writes it. Two-byte
+// accesses bound it: 16384 tokens x 80 heads of 128 bf16 from an odd address 415
+// us, where chunks of 8 bytes take 160 and of 16 bytes 119 (calls in a row).
 template <typename E>
 __global__ void rope_pairs_kernel(RopeArgs a, int64_t n) {
   const int64_t id = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
