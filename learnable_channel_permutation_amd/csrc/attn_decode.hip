@@ -29,8 +29,8 @@
 // Measured (us; bytes of K, V and scales over time), 64 heads in 8 groups of 128
 // channels unless said: 128 sequences up to 8192, bf16, 2.15 GB 340 (6.3 TB/s);
 // 2 x 131071 int8, 32 heads, 448 MB 80 (5.6); 48 up to 4096 fp8, 203 MB 45 (4.6);
-// 24 windows of 4096, 16 heads of 256, bf16, 345 MB 67 (5.1); 1 x 333 bf16, 32
-// heads of their own, 6.8 (latency). One workgroup a query head, a
+// 24 windows of 4096, 16 heads of 256, bf16, 345 MB 66 (5.2); 1 x 333 bf16, 32
+// heads of their own, 7.0 (latency). One workgroup a query head, a
 // wave a token, took 11830, 58755, 2861, 4036 and 92.
 #include <algorithm>
 
