@@ -27,9 +27,9 @@
 // the workgroups meet there.
 //
 // Measured (us; bytes of K, V and scales over time), 64 heads in 8 groups of 128
-// channels unless said: 128 sequences up to 8192, bf16, 2.15 GB 340 (6.3 TB/s);
-// 2 x 131071 int8, 32 heads, 448 MB 80 (5.6); 48 up to 4096 fp8, 203 MB 45 (4.6);
-// 24 windows of 4096, 16 heads of 256, bf16, 345 MB 66 (5.2); 1 x 333 bf16, 32
+// channels unless said: 128 sequences up to 8192, bf16, 2.15 GB 323 (6.6 TB/s);
+// 2 x 131071 int8, 32 heads, 448 MB 76 (5.9); 48 up to 4096 fp8, 203 MB 43 (4.8);
+// 24 windows of 4096, 16 heads of 256, bf16, 345 MB 63 (5.5); 1 x 333 bf16, 32
 // heads of their own, 7.0 (latency). One workgroup a query head, a
 // wave a token, took 11830, 58755, 2861, 4036 and 92.
 #include <algorithm>
@@ -75,7 +75,7 @@ __device__ __forceinline__ uint32_t codes2(uint32_t w) {
 //     the first piece is and how many there are, and the second kernel joins the
 //     pieces of each unit in order.
 struct Plan {
-  int wgs;
+  int wgs;               // workgroups launched: parts at most
   int G, tile, gu;       // query heads of a group, of a unit at most (16 HT), and units of a group
   int units;             // units of a sequence: heads * gu
   int nh;                // query heads of a unit (a group's last one may have fewer)
@@ -93,15 +93,31 @@ constexpr int kDirect = 192 << 10;
 // Cost of beginning and ending a unit, in steps: 2, 4, 8, 12 gave 53.1, 46.9, 46.4,
 // 47.7 us at 48 x 4096 fp8 and 56.5, 51.4, 50.0, 51.4 at 96 x 2048.
 constexpr int kExtra = 8;
-// Cost of a part at least, where that makes fewer than wgs: 9, 12, 16, 24 gave 20.2,
-// 16.3, 17.5, 20.6 us at 8 x 2000 bf16 and 18.2, 17.7, 18.1, 17.6 at 2 x 3000.
-constexpr uint32_t kLeast = 12;
+
+// How many parts the work is cut into, by its cost and the bytes of a step: parts of
+// 64 KB at least, and one a compute unit. A workgroup's four waves keep enough loads
+// in flight for it, and fewer streams reach more of the bandwidth; two workgroups a
+// unit pay only where conversions and unit ends, not the bytes, take the time: 8-bit
+// codes with 64 channels, or with 128 where the units are short.
+// 256 / 512 / 768 parts, us: bf16 128 x 8192 323 / 334 / 341, 24 windows of 4096 (256
+// channels) 63.3 / 66.6 / -, 1 x 131071 87.2 / 90.9 / 93.9, 64 x 8000 (64 channels)
+// 85.7 / 88.7 / 90.2; 8-bit 2 x 131071 75.3 / 78.1 / 80.0, 20 x 8000 36.3 / 36.8 /
+// 38.4, but 48 x 4096 44.4 / 42.6 / 44.6, 64 x 2000 35.8 / 32.9 / 34.5 and with 64
+// channels 128 x 8192 128 / 98 / 101, 20 x 4096 18.3 / 16.1 / 17.8. Smaller work, with
+// 768 parts of 96 KB at least against this: 1 x 131071 of one head 24.4 / 19.3, 8 x
+// 3000 22.2 / 16.8, 1 x 40000 18.8 / 15.8.
+constexpr int most_parts(int E, int D) { return E == 1 && D <= 128 ? 512 : 256; }
+template <int E, int D>
+__device__ __forceinline__ uint32_t parts_of(uint32_t all, uint32_t units) {
+  constexpr uint32_t least = (64 << 10) / (2 * kStep * D * E);
+  const bool two = most_parts(E, D) == 512 && all >= (D == 64 ? 1 : 3) * 512 * least && (D == 64 || all / 96 < units);
+  return two ? 512u : min(256u, max(1u, all / least));
+}
 
 // The cut of `all` steps.
 struct Cut {
   uint32_t parts, q, r;        // the first r parts have q + 1 steps, the others q
-  __device__ __forceinline__ Cut(uint32_t all, uint32_t wgs) {
-    parts = min(wgs, max(1u, all / kLeast));
+  __device__ __forceinline__ Cut(uint32_t all, uint32_t n) : parts(n) {
     q = all / parts;
     r = all - q * parts;
   }
@@ -183,8 +199,7 @@ struct Half {
 template <typename T>
 __device__ __forceinline__ T once(const void* p) { return __builtin_nontemporal_load((const T*)p); }
 
-// Waves per SIMD that the registers leave (checked by the compiler): what
-// hides the loads' latency, and the number of workgroups that run at a time.
+// Waves per SIMD that the registers leave (checked by the compiler).
 constexpr int waves_for(int D, int HT) { return (D == 64 ? 4 : D == 128 ? 3 : 2) - (HT - 1); }
 
 template <int FMT, int D, int HT, bool DEALT>
@@ -220,7 +235,7 @@ __global__ __launch_bounds__(256, waves_for(D, HT)) void attn_units_kernel(AttnA
     uint32_t all;
     uint32_t at = cost_before(a, per, &all, scan);
     all *= p.units;
-    cut = Cut(all, p.wgs);
+    cut = Cut(all, parts_of<E, D>(all, (uint32_t)a.B * p.units));
     // neighbouring parts on one XCD (workgroups go to the eight in turn): head
     // tiles of one key/value head then meet in its L2
     const uint32_t run = (cut.parts + 7) >> 3, rank = (blockIdx.x & 7) * run + (blockIdx.x >> 3);
@@ -625,21 +640,22 @@ Plan make_plan(const KvCache& c, int B, int hq, int max_len, int window) {
   int64_t span = max_len;
   if (window && window + (int64_t)kStep - 1 < span) span = window + (int64_t)kStep - 1;
   const bool dealt = span * c.D * (c.format == KV_BF16 ? 2 : 1) > kDirect;
-  // Two head tiles a unit where a group has them, the registers hold them and the
-  // work is enough: below it the halved number of units costs more than the bytes.
-  // One tile against two, us (32 heads a group, 2 groups): dealt, 4 / 8 / 32 x 4000
-  // 13.5 / 14.8, 21.9 / 16.9, 52.1 / 35.5 (bf16, 128), 12.9 / 14.7, 16.7 / 15.9,
-  // 34.3 / 27.7 (fp8), 12.0 / 12.5, 14.7 / 13.2, 32.8 / 25.6 (bf16, 64); direct, 64 /
-  // 256 x 500 13.1 / 13.7, 54.1 / 26.9 (bf16, 128), 8.5 / 10.7, 30.2 / 18.9 (fp8).
-  // 64 x 8192 with one group of 32, 64 heads 84.8 / 55.1, 136 / 82.
+  // Two head tiles a unit where a group has them, the registers hold them and one
+  // tile would read more than 48 MB, or (direct) leave more than a unit for each
+  // compute unit: below, half as many units cost more than the bytes. One tile
+  // against two, us (32 heads a group, 2 groups): dealt, 4 / 8 / 16 x 4000 bf16, 33 to
+  // 131 MB, 12.9 / 13.4, 14.6 / 14.7, 19.0 / 16.2; fp8, 16 to 66 MB, 11.4 / 12.9, 12.3 /
+  // 13.7, 14.6 / 14.7; 16 x 4000 of 64 int8 channels, 33 MB, 12.9 / 14.5; direct, 64 /
+  // 128 x 500 bf16 12.1 / 12.7, 19.4 / 13.5. One group of 32, 64 x 8192 bf16 48.6 / 33.5.
   const int64_t units1 = (int64_t)B * c.heads * ((p.G + 15) / 16);
-  const bool enough = dealt ? units1 * ((span + kStep - 1) / kStep) > 3 * 256 * waves_for(c.D, 1) : units1 > 256;
+  const int64_t row = 2 * c.D * (c.format == KV_BF16 ? 2 : 1);
+  const bool enough = dealt ? units1 * span * row > ((int64_t)48 << 20) : units1 > 256;
   const int HT = p.G > 16 && c.D <= 128 && enough ? 2 : 1;
   p.tile = 16 * HT;
   p.gu = (p.G + p.tile - 1) / p.tile;
   p.units = c.heads * p.gu;
   p.nh = std::min(p.G, p.tile);
-  if (dealt) p.wgs = 256 * waves_for(c.D, HT);
+  if (dealt) p.wgs = most_parts(c.format == KV_BF16 ? 2 : 1, c.D);
   return p;
 }
 
@@ -649,8 +665,7 @@ struct Space {
   size_t part, ml, cuts;       // bytes
 };
 Space space_for(const KvCache& c, int B, const Plan& p) {
-  size_t rows = (size_t)256 * waves_for(c.D, 1) * std::min(p.G, 16);
-  if (c.D <= 128) rows = std::max(rows, (size_t)256 * waves_for(c.D, 2) * std::min(p.G, 32));
+  const size_t rows = (size_t)most_parts(c.format == KV_BF16 ? 2 : 1, c.D) * std::min(p.G, c.D <= 128 ? 32 : 16);
   return {align256(2 * rows * c.D * 4), align256(2 * rows * 8),
           align256((size_t)B * c.heads * ((p.G + 15) / 16) * 8)};
 }
@@ -665,8 +680,10 @@ hipError_t run(const AttnArgs& a, const Plan& p, hipStream_t s) {
   attn_units_kernel<FMT, D, HT, true><<<(unsigned)p.wgs, 256, 0, s>>>(a, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (units * 8 <= p.wgs) {
-    const int groups = p.units * p.nh;         // eight pieces a unit and more
+  // units against rows, us: 24 units 32.2 / 20.0 (24 x 8192, 32 heads), 64 units 37.3 /
+  // 33.5 (64 x 8192), 128 units 30.0 / 30.7 (128 x 4000, 16 heads), 256 units 47.9 / 49.8
+  if (units <= 64) {
+    const int groups = p.units * p.nh;         // four pieces a unit and more, where the sequences are alike
     attn_join_kernel<D, true><<<(unsigned)(a.B * groups), 256, 0, s>>>(a, p, groups);
   } else {
     const int groups = std::min(p.units, std::max(1, 4096 / a.B));

@@ -410,6 +410,14 @@ def test_attend_groups_of_more_than_16_heads(fmt, hq, hk, D):
     check_attend(fmt, lens, hq, hk, D, 16, holes={(142, 2), (0, 0)})
 
 
+@pytest.mark.parametrize("fmt,B,n,hq,hk,D", [("fp8", 100, 4000, 4, 2, 128), ("int8", 70, 6000, 4, 2, 64),
+                                             ("bf16", 70, 3000, 2, 2, 128), ("int8", 30, 9000, 3, 1, 256)])
+def test_attend_more_work_than_one_part_a_compute_unit(fmt, B, n, hq, hk, D):
+    say("attend much work", fmt, B, n, hq, hk, D)
+    rng = np.random.default_rng(B + D)
+    check_attend(fmt, [int(x) for x in rng.integers(0, n + 1, B - 2)] + [0, n], hq, hk, D, 64)
+
+
 def test_attend_empty_batch_rows_and_zero_max_len():
     say("attend empty")
     check_attend("fp8", [0, 0, 0], 8, 2, 128, 16)
