@@ -65,7 +65,7 @@ __device__ __forceinline__ uint32_t codes2(uint32_t w) {
 // 16 HT of its query heads (HT tiles of 16, which share the loads of K and V); its
 // work is counted in steps.
 //   direct (wgs == 0): a workgroup a unit, no second kernel. Where no unit can
-//     have more than kDirect bytes of K.
+//     have more than kDirect bytes of K (kDirectMany with many units).
 //   else: the steps of all units in a row, each unit led by kExtra steps that
 //     stand for what beginning and ending it costs, cut into parts that differ
 //     by one step at most, whatever the sequences' lengths are. A workgroup finds
@@ -80,18 +80,21 @@ struct Plan {
   int units;             // units of a sequence: heads * gu
   int nh;                // query heads of a unit (a group's last one may have fewer)
   uint32_t tpm;          // ceil(2^32 / (page_size / 16)): page of a 16-token tile by a high product
+  bool space;            // whether calls of this length can be dealt: need the workspace
   float* part;           // [2 wgs][nh][D]
   float2* ml;            // [2 wgs][nh] maximum and sum
   int2* cuts;            // [B][units] place of the first piece, number of pieces
 };
-// Direct against dealt with its second kernel, us a pass: K of 128 KB (1 x 1000
-// fp8; 64 x 1000) 9.9 / 11.9; 19.9 / 24.8, 192 KB (x 1500) 12.9 / 11.7; 27.4 /
-// 30.5, 256 KB (x 2000) 16.0 / 11.8; 34.9 / 36.0. One compute unit takes in about
-// 50 KB a us, so that a direct workgroup of eight waves instead of four was slower
-// (1 x 1000: 10.9 us).
-constexpr int kDirect = 192 << 10;
-// Cost of beginning and ending a unit, in steps: 2, 4, 8, 12 gave 53.1, 46.9, 46.4,
-// 47.7 us at 48 x 4096 fp8 and 56.5, 51.4, 50.0, 51.4 at 96 x 2048.
+// Direct against dealt with its second kernel, us a pass: K of 128 KB (1 x 1000 fp8;
+// 16 x 1000; 64 x 1000) 10.2 / 10.0; 11.7 / 12.0; 20.0 / 22.5, 176 KB (x 1400) 12.5 /
+// 10.1; 14.6 / 13.0; 26.4 / 27.1, 256 KB (x 2000) 16.5 / 10.4; 19.4 / 14.4; 35.0 /
+// 33.0: up to 128 KB, and up to 192 where every compute unit has a unit. One takes in
+// about 50 KB a us, so that a direct workgroup of eight waves instead of four was
+// slower (1 x 1000: 10.9 us).
+constexpr int kDirect = 128 << 10, kDirectMany = 192 << 10;
+// Cost of beginning and ending a unit, in steps: 5, 8, 12, 18 gave 42.0, 41.9, 42.5,
+// 44.5 us at 48 x 4096 fp8, 56.0, 54.8, 57.2, 59.0 at 128 x 1000 bf16 and 17.9, 16.0,
+// 16.7, 16.8 at 12 x 3000 of 256 int8 channels.
 constexpr int kExtra = 8;
 
 // How many parts the work is cut into, by its cost and the bytes of a step: parts of
@@ -639,7 +642,9 @@ Plan make_plan(const KvCache& c, int B, int hq, int max_len, int window) {
   // the tokens a sequence can span: a window begins anywhere in a step
   int64_t span = max_len;
   if (window && window + (int64_t)kStep - 1 < span) span = window + (int64_t)kStep - 1;
-  const bool dealt = span * c.D * (c.format == KV_BF16 ? 2 : 1) > kDirect;
+  const int64_t units1 = (int64_t)B * c.heads * ((p.G + 15) / 16), row = c.D * (c.format == KV_BF16 ? 2 : 1);
+  p.space = span * row > kDirect;
+  const bool dealt = span * row > (units1 > 256 ? kDirectMany : kDirect);
   // Two head tiles a unit where a group has them, the registers hold them and one
   // tile would read more than 48 MB, or (direct) leave more than a unit for each
   // compute unit: below, half as many units cost more than the bytes. One tile
@@ -647,9 +652,7 @@ Plan make_plan(const KvCache& c, int B, int hq, int max_len, int window) {
   // 131 MB, 12.9 / 13.4, 14.6 / 14.7, 19.0 / 16.2; fp8, 16 to 66 MB, 11.4 / 12.9, 12.3 /
   // 13.7, 14.6 / 14.7; 16 x 4000 of 64 int8 channels, 33 MB, 12.9 / 14.5; direct, 64 /
   // 128 x 500 bf16 12.1 / 12.7, 19.4 / 13.5. One group of 32, 64 x 8192 bf16 48.6 / 33.5.
-  const int64_t units1 = (int64_t)B * c.heads * ((p.G + 15) / 16);
-  const int64_t row = 2 * c.D * (c.format == KV_BF16 ? 2 : 1);
-  const bool enough = dealt ? units1 * span * row > ((int64_t)48 << 20) : units1 > 256;
+  const bool enough = dealt ? units1 * span * 2 * row > ((int64_t)48 << 20) : units1 > 256;
   const int HT = p.G > 16 && c.D <= 128 && enough ? 2 : 1;
   p.tile = 16 * HT;
   p.gu = (p.G + p.tile - 1) / p.tile;
@@ -704,7 +707,7 @@ hipError_t run_d(const AttnArgs& a, const Plan& p, hipStream_t s) {
 size_t attn_workspace_bytes(const KvCache& c, int B, int hq, int max_len, int window) {
   const Plan p = make_plan(c, B, hq, max_len, window);
   const Space n = space_for(c, B, p);
-  return p.wgs ? n.part + n.ml + n.cuts : 0;
+  return p.space ? n.part + n.ml + n.cuts : 0;
 }
 
 hipError_t launch_attn_decode(const AttnArgs& a, hipStream_t s) {
