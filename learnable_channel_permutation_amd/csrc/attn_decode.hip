@@ -577,7 +577,7 @@ __global__ __launch_bounds__(256, waves_for(D, HT)) void attn_units_kernel(AttnA
 // workgroup per query head, its thread groups share the pieces (few units of
 // many pieces); else a sequence's units go over `groups` workgroups, a thread
 // group takes a head at a time. Its three reads in a row (lengths, cuts, pieces)
-// bound it: 4.7 us with 2 to 6 MB of pieces.
+// bound it: 4.5 us with 1 to 3 MB of pieces.
 template <int D, bool ROWS>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, Plan p, int groups) {
   constexpr int TG = 256 / (D / 4);            // thread groups
