@@ -523,7 +523,8 @@ int lcp_kv_read(const lcp_kv_cache* c, const int32_t* slots, int T, void* k_out,
  *   out: [B][hq][D] in odt (F32 or BF16), 16-byte aligned; lse (nullable):
  *   [B][hq] fp32. scale finite. window >= 0.
  *   ws: lcp_attn_decode_workspace_bytes bytes, 256-byte aligned (NULL where that
- *   is 0); one workspace serves one call in flight. */
+ *   is 0); one workspace serves one call in flight, and one for a batch and a
+ *   max_len serves smaller ones. */
 int lcp_attn_decode_workspace_bytes(const lcp_kv_cache* c, int B, int hq,
                                     int max_len, int window, size_t* bytes);
 int lcp_attn_decode(const lcp_kv_cache* c, const void* q, int64_t q_row, int B,
