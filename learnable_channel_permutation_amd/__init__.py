@@ -115,13 +115,17 @@ class LayerSession:
         return errs
 
 
-
-def _used_on(stream, t):
-    """A new tensor that a call on `stream` (None: the current one, which torch
-    orders by itself) uses: its memory is not given away before that stream is done with it."""
-    if stream is not None:
-        t.record_stream(stream)
-    return t
+def _made_on(stream, given, call, *args):
+    """call(*args, None) with `stream` as the current one, so that what it allocates belongs to that stream: a block
+    of the caller's stream may still be in use by work queued there, which `stream` does not wait for. The tensors
+    that it makes (results not among `given`) are kept from reuse until the caller's stream is done with them, too."""
+    caller = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        results = call(*args, None)
+    for t in results[1:]:
+        if t is not None and not any(t is g for g in given):
+            t.record_stream(caller)
+    return results
 
 
 class PagedKVCache:
@@ -155,28 +159,20 @@ class PagedKVCache:
 
     def read(self, slots, k_out=None, v_out=None, stream=None):
         """The stored k and v of slots, [T, heads, D] bfloat16 unless outputs are given (lcp_kv_read)."""
-        if stream is not None and k_out is None:
-            k_out = _used_on(stream, slots.new_empty((slots.shape[0], self.c.heads, self.c.D), dtype=torch.bfloat16))
-        if stream is not None and v_out is None:
-            v_out = _used_on(stream, torch.empty_like(k_out))
-        code, k_out, v_out = _lib._serve.read(self.c, slots, k_out, v_out, stream)
+        if stream is None or (k_out is not None and v_out is not None):
+            code, k_out, v_out = _lib._serve.read(self.c, slots, k_out, v_out, stream)
+        else:
+            code, k_out, v_out = _made_on(stream, (k_out, v_out), _lib._serve.read, self.c, slots, k_out, v_out)
         _lib._check("lcp_kv_read", code)
         return k_out, v_out
 
     def attend(self, q, pages, lens, max_len=None, scale=None, window=0, out=None, lse=None, ws=None, stream=None):
         """Attention of one new token of each sequence, q [B, hq, D] bfloat16 (lcp_attn_decode): (out, lse). max_len,
         the host's bound on lens, defaults to what the page table can hold; scale to D^-1/2."""
-        if stream is not None:
-            if max_len is None:
-                max_len = pages.shape[1] * self.c.page_size
-            if out is None:
-                out = _used_on(stream, torch.empty_like(q, memory_format=torch.contiguous_format))
-            if lse is None:
-                lse = _used_on(stream, q.new_empty(q.shape[:2], dtype=torch.float32))
-            if ws is None:
-                n = lcp_attn_decode_workspace_bytes(self.c, q.shape[0], q.shape[1], max_len, window)
-                ws = _used_on(stream, q.new_empty(n, dtype=torch.uint8)) if n else None
-        code, out, lse = _lib._serve.attend(self.c, q, pages, lens, max_len, out, lse, ws, scale, window, True,
-                                            stream)
+        args = (self.c, q, pages, lens, max_len, out, lse, ws, scale, window, True)
+        if stream is None or (out is not None and lse is not None and ws is not None):
+            code, out, lse = _lib._serve.attend(*args, stream)
+        else:
+            code, out, lse = _made_on(stream, (out, lse), _lib._serve.attend, *args)
         _lib._check("lcp_attn_decode", code)
         return out, lse
