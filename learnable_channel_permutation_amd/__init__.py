@@ -136,11 +136,18 @@ class PagedKVCache:
     128 or 256, page_size a multiple of 16. Which pages belong to which
     sequence is the caller's: slots (page * page_size + offset) say where new
     tokens go, a page table [B, max_pages] and the lengths what a step reads.
+    The tensors are the cache's for its life: k, v, k_scale and v_scale are read-only.
     """
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.c = make_kv_cache(k, v, k_scale, v_scale)
+        self._c = make_kv_cache(k, v, k_scale, v_scale)
+
+    # The tensors and the struct of their addresses are one: another tensor needs another cache.
+    c = property(lambda self: self._c)
+    k = property(lambda self: self._c.tensors[0])
+    v = property(lambda self: self._c.tensors[1])
+    k_scale = property(lambda self: self._c.tensors[2])
+    v_scale = property(lambda self: self._c.tensors[3])
 
     @classmethod
     def empty(cls, pages, page_size, heads, D, dtype=torch.float8_e4m3fn, device="cuda"):
@@ -154,22 +161,22 @@ class PagedKVCache:
     def append(self, k, v, slots, q=None, q_out=None, table=None, pos=None, interleaved=False, stream=None):
         """Write new tokens' k and v [T, heads, D] (k rotated by the table at pos first) and rotate q [T, hq, D]
         into q_out (lcp_kv_append)."""
-        lcp_kv_append(self.c, k, v, slots, q, q_out, table, pos, interleaved, stream)
+        lcp_kv_append(self._c, k, v, slots, q, q_out, table, pos, interleaved, stream)
         return q_out
 
     def read(self, slots, k_out=None, v_out=None, stream=None):
         """The stored k and v of slots, [T, heads, D] bfloat16 unless outputs are given (lcp_kv_read)."""
         if stream is None or (k_out is not None and v_out is not None):
-            code, k_out, v_out = _lib._serve.read(self.c, slots, k_out, v_out, stream)
+            code, k_out, v_out = _lib._serve.read(self._c, slots, k_out, v_out, stream)
         else:
-            code, k_out, v_out = _made_on(stream, (k_out, v_out), _lib._serve.read, self.c, slots, k_out, v_out)
+            code, k_out, v_out = _made_on(stream, (k_out, v_out), _lib._serve.read, self._c, slots, k_out, v_out)
         _lib._check("lcp_kv_read", code)
         return k_out, v_out
 
     def attend(self, q, pages, lens, max_len=None, scale=None, window=0, out=None, lse=None, ws=None, stream=None):
         """Attention of one new token of each sequence, q [B, hq, D] bfloat16 (lcp_attn_decode): (out, lse). max_len,
         the host's bound on lens, defaults to what the page table can hold; scale to D^-1/2."""
-        args = (self.c, q, pages, lens, max_len, out, lse, ws, scale, window, True)
+        args = (self._c, q, pages, lens, max_len, out, lse, ws, scale, window, True)
         if stream is None or (out is not None and lse is not None and ws is not None):
             code, out, lse = _lib._serve.attend(*args, stream)
         else:

@@ -92,6 +92,7 @@ class lcp_kv_cache(ctypes.Structure):
                 ("v_scale", ctypes.c_void_p), ("format", ctypes.c_int), ("pages", ctypes.c_int),
                 ("page_size", ctypes.c_int), ("heads", ctypes.c_int), ("D", ctypes.c_int)]
     gpu = -2                # the device index of its tensors (-1: the CPU's), -2: not known
+    tensors = None          # the tensors whose addresses it holds, kept alive with it (make_kv_cache)
 
 
 class LcpError(RuntimeError):
@@ -393,6 +394,7 @@ def make_kv_cache(k, v, k_scale=None, v_scale=None):
     formats, scales [pages, heads, page_size]."""
     c = lcp_kv_cache.from_buffer_copy(_serve.cache(k, v, k_scale, v_scale))
     c.gpu = k.get_device()
+    c.tensors = (k, v, k_scale, v_scale)
     return c
 
 

@@ -221,3 +221,30 @@ def test_table_on_the_cpu_is_refused():
     L = _lib()
     with pytest.raises(ValueError, match="on the GPU"):
         L.lcp_rope_table(L.make_rope_cfg(64), torch.zeros(9, 32, 2))
+
+
+def test_cache_and_its_addresses_stay_together():
+    """No call may use the address of a tensor that was replaced or freed."""
+    import gc
+    import weakref
+    import learnable_channel_permutation_amd as lcp
+    L = _lib()
+
+    def tensors(pages):
+        k, s = torch.zeros(pages, 2, 16, 64, dtype=torch.int8), torch.zeros(pages, 2, 16)
+        return k, k.clone(), s, s.clone()
+
+    c = lcp.PagedKVCache(*tensors(4))
+    for name, t in zip(("k", "v", "k_scale", "v_scale"), tensors(9)):
+        with pytest.raises(AttributeError):
+            setattr(c, name, t)
+        assert getattr(c.c, name) == getattr(c, name).data_ptr()
+    with pytest.raises(AttributeError):
+        c.c = L.make_kv_cache(*tensors(9))
+    all4 = tensors(4)
+    alive = [weakref.ref(t) for t in all4]
+    s = L.make_kv_cache(*all4)
+    del all4
+    gc.collect()
+    assert all(r() is not None and r().data_ptr() == getattr(s, n)
+               for r, n in zip(alive, ("k", "v", "k_scale", "v_scale")))
