@@ -449,7 +449,7 @@ int lcp_rope_table(const lcp_rope_cfg* rc, int max_pos, float* table, void* stre
  *   a' = a c - b s,  b' = b c + a s;     inverse != 0: s taken as -s.
  * inverse = 1 is the transpose, so it turns dL/dy into dL/dx (the gradient, and
  * the inverse rotation for magnitude 1). Channels from rot_dim on are copied.
- * fp32 arithmetic, one rounding to dt.
+ * fp32 arithmetic (each product and the sum rounded by itself), one rounding to dt.
  *   dt F32 or BF16; D in 2 .. 1024, rot_dim even, 2 .. D; pos[t] is held to
  *   [0, max_pos - 1]; strides of y must keep its rows apart. */
 int lcp_rope(const lcp_heads* q, const lcp_heads* k, lcp_dtype dt, int T, int D,
@@ -484,7 +484,7 @@ typedef struct lcp_kv_cache {
 
 /* lcp_kv_append - write T tokens' keys and values into the cache, quantised to
  * its format, and rotate their queries, in one launch. With a table, K is
- * rotated first (lcp_rope's rotation, in fp32, not rounded before it is
+ * rotated first (lcp_rope's rotation, to the same bits, in fp32, not rounded before it is
  * quantised) and q (nullable) is rotated into q->y; without a table (NULL) K is
  * stored as it is and q must be NULL.
  *   q, k, v: bf16 head rows; k->heads = v->heads = the cache's; k->y and v->y

@@ -8,18 +8,6 @@ namespace {
 // fp32 -> one e4m3 code (nearest even); |v| <= 448 or NaN
 __device__ __forceinline__ uint32_t to_e4m3(float v) { return __builtin_amdgcn_cvt_pk_fp8_f32(v, v, 0, false) & 0xff; }
 
-// The rotation with two rounded products and one rounded sum, never a fused
-// multiply-add: the 8-bit codes then follow from the definition in fp32 to the
-// last bit, however this is compiled.
-__device__ __forceinline__ float rot_first(float a, float b, float c, float s) {
-#pragma clang fp contract(off)
-  return a * c - b * s;
-}
-__device__ __forceinline__ float rot_second(float a, float b, float c, float s) {
-#pragma clang fp contract(off)
-  return b * c + a * s;
-}
-
 // Scale of a row with maximum magnitude bits `a` (the bits of max |x|; a NaN
 // has the largest). Not finite: NaN.
 __device__ __forceinline__ float row_scale(uint32_t a, int format) {

@@ -65,8 +65,8 @@ __global__ void rope_pairs_kernel(RopeArgs a, int64_t n) {
   const float s = a.inverse ? -cs.y : cs.y;
   const int d0 = a.interleaved ? 2 * i : i, d1 = a.interleaved ? 2 * i + 1 : i + half;
   const float u = load<E>(r.x, x + d0), v = load<E>(r.x, x + d1);
-  store(out, y + d0, u * cs.x - v * s);
-  store(out, y + d1, v * cs.x + u * s);
+  store(out, y + d0, rot_first(u, v, cs.x, s));
+  store(out, y + d1, rot_second(u, v, cs.x, s));
 }
 
 // One thread per (token, head, unit). A unit is 2 V channels of a head row, V
@@ -116,8 +116,8 @@ __global__ __launch_bounds__(256) void rope_units_kernel(RopeArgs a, int64_t n) 
         float& u0 = f[a.interleaved ? 2 * (j + i) : j + i];
         float& u1 = f[a.interleaved ? 2 * (j + i) + 1 : j + i + V];
         const float c = cs[2 * i], s = a.inverse ? -cs[2 * i + 1] : cs[2 * i + 1], p0 = u0, p1 = u1;
-        u0 = p0 * c - p1 * s;
-        u1 = p1 * c + p0 * s;
+        u0 = rot_first(p0, p1, c, s);
+        u1 = rot_second(p0, p1, c, s);
       }
     }
     w0 = C::pack(f);

@@ -46,6 +46,18 @@ struct RopeChunk<float, 4> {
   static __device__ __forceinline__ T pack(const float* f) { return T{f[0], f[1], f[2], f[3]}; }
 };
 
+// The rotation of a pair (a, b) with two rounded products and one rounded sum, never
+// a fused multiply-add: every kernel that rotates gives the same bits, and the 8-bit
+// codes of keys follow from the definition in fp32, however this is compiled.
+__device__ __forceinline__ float rot_first(float a, float b, float c, float s) {
+#pragma clang fp contract(off)
+  return a * c - b * s;
+}
+__device__ __forceinline__ float rot_second(float a, float b, float c, float s) {
+#pragma clang fp contract(off)
+  return b * c + a * s;
+}
+
 // Loads and stores of data that nobody finds in the caches again: a call that
 // moves more than the 256 MB of the last-level cache hints them as streaming.
 // Measured on the rotary kernel (72 heads of 128 bf16) with a kernel that reads
