@@ -13,17 +13,21 @@ namespace {
 inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 inline bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }      // index arrays
 inline hipStream_t S(void* s) { return reinterpret_cast<hipStream_t>(s); }
-constexpr int64_t kMaxStride = (int64_t)1 << 40;   // keeps every element offset far inside 64 bits
+constexpr int64_t kMaxStride = (int64_t)1 << 40;
+// Elements from one side of a tensor to the other along an axis: every offset and sum of offsets then stays inside 64 bits.
+constexpr int64_t kMaxSpan = (int64_t)1 << 60;
 
 // Input rows: pointer, head count and strides. Rows may share memory (a
 // broadcast input has stride 0).
-bool good_rows_in(const lcp_heads* h) {
+bool good_rows_in(const lcp_heads* h, int T) {
   return h->x && h->heads >= 1 && h->heads <= 65536 && h->x_token >= 0 && h->x_head >= 0 && h->x_token <= kMaxStride &&
-         h->x_head <= kMaxStride;
+         h->x_head <= kMaxStride && h->x_token <= kMaxSpan / T;
 }
 // Output rows must not overlap each other: either nesting of the two strides.
 bool good_rows_out(const lcp_heads* h, int T, int D) {
-  if (!h->y || h->y_token < 0 || h->y_head < 0 || h->y_token > kMaxStride || h->y_head > kMaxStride) return false;
+  if (!h->y || h->y_token < 0 || h->y_head < 0 || h->y_token > kMaxStride || h->y_head > kMaxStride ||
+      h->y_token > kMaxSpan / T)
+    return false;
   const int64_t H = h->heads;
   if (h->y == h->x && (h->x_token != h->y_token || h->x_head != h->y_head) && !(T == 1 && h->x_head == h->y_head) &&
       !(H == 1 && h->x_token == h->y_token) && !(T == 1 && H == 1))
@@ -107,7 +111,7 @@ int lcp_rope(const lcp_heads* q, const lcp_heads* k, lcp_dtype dt, int T, int D,
   const uintptr_t es = dt == LCP_BF16 ? 1 : 3;
   for (const lcp_heads* h : {q, k}) {
     if (!h) continue;
-    if (!good_rows_in(h) || !good_rows_out(h, T, D)) return LCP_E_INVAL;
+    if (!good_rows_in(h, T) || !good_rows_out(h, T, D)) return LCP_E_INVAL;
     if (((uintptr_t)h->x & es) != 0 || ((uintptr_t)h->y & es) != 0) return LCP_E_INVAL;
   }
   const int64_t rows = (int64_t)T * (q->heads + (k ? k->heads : 0));
@@ -131,10 +135,10 @@ int lcp_kv_append(const lcp_kv_cache* c, const lcp_heads* q, const lcp_heads* k,
   int rc = check_cache(c, &a.c);
   if (rc != LCP_OK) return rc;
   if (!k || !v || !slots || T <= 0 || !aligned4(slots)) return LCP_E_INVAL;
-  if (!good_rows_in(k) || !good_rows_in(v) || k->heads != c->heads || v->heads != c->heads) return LCP_E_INVAL;
+  if (!good_rows_in(k, T) || !good_rows_in(v, T) || k->heads != c->heads || v->heads != c->heads) return LCP_E_INVAL;
   if (((uintptr_t)k->x & 1) != 0 || ((uintptr_t)v->x & 1) != 0) return LCP_E_INVAL;
   if (q) {
-    if (!table || !good_rows_in(q) || !good_rows_out(q, T, c->D)) return LCP_E_INVAL;
+    if (!table || !good_rows_in(q, T) || !good_rows_out(q, T, c->D)) return LCP_E_INVAL;
     if (((uintptr_t)q->x & 1) != 0 || ((uintptr_t)q->y & 1) != 0) return LCP_E_INVAL;
   }
   if (table) {

@@ -248,3 +248,17 @@ def test_cache_and_its_addresses_stay_together():
     gc.collect()
     assert all(r() is not None and r().data_ptr() == getattr(s, n)
                for r, n in zip(alive, ("k", "v", "k_scale", "v_scale")))
+
+
+def test_strides_whose_span_passes_64_bits_are_refused():
+    """Sums of offsets that wrap would pass for rows that keep apart: token 2 and head 1 meet here."""
+    L = _lib()
+    T = (1 << 25) + 1
+    for kw in (dict(yt=1 << 39, yh=1 << 40), dict(xt=1 << 39)):
+        q = ctypes.byref(_rows(L, **kw))
+        assert L.LIB.lcp_rope(q, None, L.LCP_BF16, T, 128, P, 10, P, 128, 0, 0, None) == L.LCP_E_INVAL
+        k = ctypes.byref(_rows(L, xt=1 << 39))
+        good = ctypes.byref(_rows(L))
+        for a in ((q, good, good), (None, k, good), (None, good, k)):
+            assert L.LIB.lcp_kv_append(ctypes.byref(_cache(L, heads=4)), *a, T >> 1, P, P, 10, P, 128, 0,
+                                       None) == L.LCP_E_INVAL
