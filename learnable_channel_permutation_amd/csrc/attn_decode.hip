@@ -599,7 +599,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, Plan p, int 
     const int pieces = some ? uniform((const int*)p.cuts, 2 * unit + 1) : 0;
     if (pieces == 1) continue;                 // written whole by its workgroup
     const int h0 = u % p.gu * p.tile, nh = min(p.tile, p.G - h0);
-    for (int h = ROWS ? group % p.nh : tg; h < nh; h += ROWS ? nh : TG) {
+    for (int h = ROWS ? group % p.nh : tg; h < nh; h += ROWS ? p.nh : TG) {        // one writer a row
       float M = kLowest, L = 0.f;
       f32x4 y = {0.f, 0.f, 0.f, 0.f};
       for (int i = ROWS ? tg : 0; i < pieces; i += 4 * STEP) {
