@@ -270,6 +270,7 @@ hipError_t run_append_d(const KvAppendArgs& a, hipStream_t s) {
 template <int FMT, bool BF>
 hipError_t run_read(const KvCache& c, const int* slots, int T, void* k, void* v, hipStream_t s) {
   const int64_t n = (int64_t)T * c.heads * (c.D / 8), grid = (n + 255) / 256;
+  if (n > kMaxThreads) return hipErrorInvalidConfiguration;
   const bool stream = n * 16 * ((FMT == KV_BF16 ? 2 : 1) + (BF ? 2 : 4)) > kStreamBytes;
   if (stream) kv_read_kernel<FMT, BF, true><<<(unsigned)grid, 256, 0, s>>>(c, slots, n, (char*)k, (char*)v);
   else kv_read_kernel<FMT, BF, false><<<(unsigned)grid, 256, 0, s>>>(c, slots, n, (char*)k, (char*)v);

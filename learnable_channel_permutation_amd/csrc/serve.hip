@@ -169,7 +169,6 @@ int lcp_kv_read(const lcp_kv_cache* c, const int32_t* slots, int T, void* k_out,
   if (!slots || T <= 0 || !aligned4(slots) || !k_out || !v_out || k_out == v_out) return LCP_E_INVAL;
   if (odt != LCP_F32 && odt != LCP_BF16) return LCP_E_UNSUPPORTED;
   if (!aligned16(k_out) || !aligned16(v_out)) return LCP_E_INVAL;
-  if ((int64_t)T * c->heads >= ((int64_t)1 << 31) / 32) return LCP_E_INVAL;
   LCP_RUN(launch_kv_read(kc, slots, T, k_out, v_out, odt == LCP_BF16, S(stream)));
   return LCP_OK;
 }
