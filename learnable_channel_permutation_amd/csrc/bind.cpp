@@ -61,6 +61,12 @@ int small(PyObject* o) {
   return (int)v;
 }
 
+int flag(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Bad{nullptr};
+  return v;
+}
+
 // The package's function from a stream argument (None: the current stream) to a
 // handle; called once the arguments are known to be good.
 PyObject* handle_of = nullptr;
@@ -175,8 +181,8 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor &tab = tensor(a[2], "table must be a tensor"), &at_pos = tensor(a[3], "pos must be a tensor");
     const Table t = table_of(tab);
     const int32_t* pos = index_of(at_pos, T, "pos must be contiguous int32 [T]");
+    const int inter = flag(a[6]), inverse = flag(a[7]);
     const int gpu = on_gpu({&q, &qo, k, ko, &tab, &at_pos});
-    const int inter = PyObject_IsTrue(a[6]), inverse = PyObject_IsTrue(a[7]);
     void* s = stream_of(a[8], gpu);
     int code;
     Py_BEGIN_ALLOW_THREADS
@@ -248,8 +254,8 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     const at::Tensor& at_slots = tensor(a[3], "slots must be a tensor");
     const int32_t* slots = index_of(at_slots, T, "slots must be contiguous int32 [T]");
+    const int inter = flag(a[8]);
     const int gpu = on_gpu({&k, &v, q, qo, tab, tab ? &THPVariable_Unpack(a[7]) : nullptr, &at_slots}, c.gpu);
-    const int inter = PyObject_IsTrue(a[8]);
     void* s = stream_of(a[9], gpu);
     int code;
     Py_BEGIN_ALLOW_THREADS
@@ -328,7 +334,7 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int max_len = most < 0 ? -1 : (int)most, window = small(a[9]);
     const double scale = a[8] == Py_None ? 1.0 / std::sqrt((double)D) : PyFloat_AsDouble(a[8]);
     if (scale == -1.0 && PyErr_Occurred()) return nullptr;
-    const bool make = PyObject_IsTrue(a[10]);
+    const bool make = flag(a[10]);
     if (!make && !out) throw Bad{"out must be a tensor"};
     size_t need = 0;
     int code = lcp_attn_decode_workspace_bytes(c.get(), B, hq, max_len, window, &need);

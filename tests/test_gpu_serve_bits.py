@@ -51,3 +51,12 @@ def test_every_rotation_gives_the_bits_of_the_fp32_definition(D, rot, interleave
         out = torch.empty_like(q)
         cache.append(kv, kv, slots, q=inp, q_out=out, table=dt, pos=dp, interleaved=interleaved)
         assert torch.equal(out, want)
+
+
+def test_a_flag_without_a_truth_value_is_its_own_error():
+    say("flags")
+    x, t = torch.zeros(3, 2, 64, dtype=torch.bfloat16, device=DEV), torch.zeros(9, 32, 2, device=DEV)
+    pos = torch.zeros(3, dtype=torch.int32, device=DEV)
+    for kw in (dict(interleaved=torch.ones(2)), dict(inverse=torch.ones(2))):
+        with pytest.raises(RuntimeError, match="ambiguous"):
+            lcp.lcp_rope(x, torch.empty_like(x), t, pos, **kw)

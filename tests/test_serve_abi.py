@@ -262,3 +262,17 @@ def test_strides_whose_span_passes_64_bits_are_refused():
         for a in ((q, good, good), (None, k, good), (None, good, k)):
             assert L.LIB.lcp_kv_append(ctypes.byref(_cache(L, heads=4)), *a, T >> 1, P, P, 10, P, 128, 0,
                                        None) == L.LCP_E_INVAL
+
+
+def test_a_flag_without_a_truth_value_is_its_own_error():
+    """As any Python call reports it; not a result with an error left behind."""
+    import learnable_channel_permutation_amd as lcp
+    x, t = torch.zeros(3, 2, 64, dtype=torch.bfloat16), torch.zeros(9, 32, 2)
+    pos, both = torch.zeros(3, dtype=torch.int32), torch.ones(2)
+    k, s = torch.zeros(4, 2, 16, 64, dtype=torch.int8), torch.zeros(4, 2, 16)
+    c = lcp.PagedKVCache(k, k.clone(), s, s.clone())
+    for call in (lambda: lcp.lcp_rope(x, torch.empty_like(x), t, pos, interleaved=both),
+                 lambda: lcp.lcp_rope(x, torch.empty_like(x), t, pos, inverse=both),
+                 lambda: c.append(x, x, pos, table=t, pos=pos, interleaved=both)):
+        with pytest.raises(RuntimeError, match="ambiguous"):
+            call()
