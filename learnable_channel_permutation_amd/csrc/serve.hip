@@ -148,8 +148,8 @@ int lcp_kv_append(const lcp_kv_cache* c, const lcp_heads* q, const lcp_heads* k,
   }
   if ((int64_t)T * ((q ? q->heads : 0) + 2 * (int64_t)c->heads) >= ((int64_t)1 << 31)) return LCP_E_INVAL;
   if (q) a.q = rows_of(q);
-  a.k = rows_of(k);
-  a.v = rows_of(v);
+  a.k = Rows{k->x, nullptr, k->heads, k->x_token, k->x_head, 0, 0};       // their y is not used
+  a.v = Rows{v->x, nullptr, v->heads, v->x_token, v->x_head, 0, 0};
   a.T = T;
   a.rot = table ? rot_dim : 0;
   a.max_pos = max_pos;
