@@ -19,7 +19,7 @@ from ._lib import (LCP_BF16, LCP_F32, LcpError, lcp_colnorm, lcp_error,  # noqa:
                    lcp_rope_table, make_kv_cache, make_rope_cfg, lcp_deploy_forward, lcp_gather_channels,
                    lcp_layer_outputs_noalloc, lcp_sparse_gemm, lcp_sparse_pack, lcp_sparse_pack_bytes)
 
-__all__ = ["LayerSession", "LcpError", "PagedKVCache"] + [n for n in _lib.EXPORTS if n.startswith("lcp_")]
+__all__ = ["LayerSession", "LcpError", "PagedKVCache"] + [n for n in _lib.EXPORTS if n in globals()]
 
 
 class LayerSession:

@@ -276,3 +276,12 @@ def test_a_flag_without_a_truth_value_is_its_own_error():
                  lambda: c.append(x, x, pos, table=t, pos=pos, interleaved=both)):
         with pytest.raises(RuntimeError, match="ambiguous"):
             call()
+
+
+def test_every_public_name_exists():
+    import learnable_channel_permutation_amd as lcp
+    names = {}
+    exec("from learnable_channel_permutation_amd import *", names)
+    assert set(lcp.__all__) <= set(names)
+    # the two that have no Python form of their own: messages come with LcpError, the version is the library's
+    assert set(_lib().EXPORTS) - set(lcp.__all__) == {"lcp_status_string", "lcp_version"}
