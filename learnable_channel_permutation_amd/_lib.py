@@ -4,8 +4,8 @@ Argument marshalling only, for the serving calls by the native module _serve
 (csrc/bind.cpp), for the others here: tensors become device pointers, dtypes become
 lcp_dtype codes, the current torch stream becomes the HIP stream; every step
 of the computation runs in the library's kernels. A non-zero status raises
-LcpError. If the shared library is missing this module raises at import:
-there is no fallback path.
+LcpError. Without liblcp.so this module raises at import, without _serve.so the
+serving calls raise: there is no fallback path.
 """
 from __future__ import annotations
 
@@ -155,7 +155,23 @@ def _load():
 
 
 LIB = _load()
-from . import _serve  # noqa: E402  (built beside liblcp.so, which it calls; needs torch imported)
+
+
+class _NotLoaded:
+    """Stands for the native module of the serving calls where it cannot be loaded: only those calls need it."""
+
+    def __init__(self, why):
+        self.why = why
+
+    def __getattr__(self, name):
+        raise ImportError("the serving calls need _serve.so beside liblcp.so, built for this Python and torch by "
+                          "learnable_channel_permutation_amd/build.py (%s)" % self.why)
+
+
+try:
+    from . import _serve  # built beside liblcp.so, which it calls; needs torch imported
+except ImportError as e:
+    _serve = _NotLoaded(e)
 
 _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
@@ -175,8 +191,7 @@ def _p(t):
 
 
 def _stream(stream=None):
-    """The HIP stream handle: the given stream's, or the current one of the current device (asked for by its raw
-    handle, which takes a twentieth of the time of building torch's stream object)."""
+    """The HIP stream handle: the given stream's, or the current one of the current device."""
     if stream is None:
         return _raw_stream(_current_device())
     return stream.cuda_stream
@@ -365,7 +380,8 @@ def lcp_deploy_forward(vals, meta, perm, B, X, cout, Xp, Y, stream=None):
 
 
 # ---- serving operators --------------------------------------------------------
-_serve.use_streams(_stream)
+if not isinstance(_serve, _NotLoaded):
+    _serve.use_streams(_stream)
 
 
 def make_rope_cfg(rot_dim, base=10000.0, scaling="none", factor=1.0, orig_len=0.0, low_turns=1.0, high_turns=32.0,

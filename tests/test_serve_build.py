@@ -1,0 +1,34 @@
+"""What the serving calls' native module asks of everyone else: nothing (no GPU)."""
+import os
+import shutil
+import subprocess
+import sys
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+PKG = os.path.join(ROOT, "learnable_channel_permutation_amd")
+
+
+def python(code, cwd):
+    p = subprocess.run([sys.executable, "-c", code], cwd=cwd, capture_output=True, text=True, timeout=300)
+    assert p.returncode == 0, p.stdout + p.stderr
+    return p.stdout
+
+
+def test_the_package_works_without_the_serving_module(tmp_path):
+    """Learning and deploying need liblcp.so alone; a serving call says what is missing."""
+    shutil.copytree(PKG, tmp_path / "learnable_channel_permutation_amd",
+                    ignore=shutil.ignore_patterns("_serve.so", "__pycache__", "csrc"))
+    out = python('''
+import torch
+import learnable_channel_permutation_amd as lcp
+assert lcp.lcp_xt_pitch(100) >= 100 and lcp.lcp_sparse_pack_bytes(64, 64)[0] > 0 and lcp.LayerSession
+x, i = torch.zeros(1, 1, 64), torch.zeros(1, dtype=torch.int32)
+for call in (lambda: lcp.lcp_rope(x, x, x, i), lambda: lcp.PagedKVCache.empty(1, 16, 1, 64, device="cpu"),
+             lambda: lcp.lcp_kv_append(None, x, x, i)):
+    try:
+        call()
+    except ImportError as e:
+        assert "_serve.so" in str(e) and "build.py" in str(e)
+        print("told")
+''', tmp_path)
+    assert out.split() == ["told"] * 3
