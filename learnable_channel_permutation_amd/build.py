@@ -1,5 +1,6 @@
 """Build liblcp.so (gfx950) in-tree from csrc/*.hip with hipcc, and _serve.so,
-the marshalling of the serving calls, from csrc/bind.cpp with g++.
+the marshalling of the serving calls, from csrc/bind.cpp with g++ (where that
+fails, the build does, but liblcp.so is there for every other call).
 
     python learnable_channel_permutation_amd/build.py
 
@@ -9,7 +10,6 @@ invocation recompiles every source.
 from __future__ import annotations
 
 import concurrent.futures as cf
-import importlib.util
 import os
 import subprocess
 import sys
@@ -56,11 +56,13 @@ def _compile(src):
 
 
 def _compile_bind():
-    """csrc/bind.cpp against the headers of Python and torch (torch itself is not imported)."""
-    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    """csrc/bind.cpp against the headers of Python and torch, with torch's C++ ABI."""
+    import torch as t
+    torch = os.path.dirname(t.__file__)
     obj = os.path.join(OBJ, "host", "bind.o")        # apart from the library's objects
     os.makedirs(os.path.dirname(obj), exist_ok=True)
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-isystem", os.path.join(torch, "include"), "-isystem",
+    abi = "-D_GLIBCXX_USE_CXX11_ABI=%d" % t.compiled_with_cxx11_abi()
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", abi, "-isystem", os.path.join(torch, "include"), "-isystem",
            os.path.join(torch, "include", "torch", "csrc", "api", "include"), "-isystem",
            sysconfig.get_paths()["include"], "-c", os.path.join(CSRC, "bind.cpp"), "-o", obj]
     p = subprocess.run(cmd, capture_output=True, text=True)
@@ -86,14 +88,16 @@ def build(verbose=False):
     with cf.ThreadPoolExecutor(max_workers=workers) as ex:
         bind = ex.submit(_compile_bind)
         objs = list(ex.map(_compile, srcs))
-        bind = bind.result()
     tmp = LIB + ".tmp"
     cmd = [_hipcc(), "--offload-arch=" + ARCH, "-shared", "-fPIC", "-o", tmp] + objs
     p = subprocess.run(cmd, capture_output=True, text=True)
     if p.returncode != 0:
         raise RuntimeError("link failed:\n%s" % p.stderr)
     os.replace(tmp, LIB)
-    _link_bind(*bind)
+    # after the library, which works without it, but not with an older one
+    if os.path.exists(BIND):
+        os.remove(BIND)
+    _link_bind(*bind.result())
     if verbose:
         print("built", LIB, "and", BIND)
     return LIB

@@ -1,8 +1,11 @@
 """What the serving calls' native module asks of everyone else: nothing (no GPU)."""
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+
+import pytest
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 PKG = os.path.join(ROOT, "learnable_channel_permutation_amd")
@@ -32,3 +35,36 @@ for call in (lambda: lcp.lcp_rope(x, x, x, i), lambda: lcp.PagedKVCache.empty(1,
         print("told")
 ''', tmp_path)
     assert out.split() == ["told"] * 3
+
+
+def test_the_library_is_built_where_the_serving_module_cannot_be(tmp_path, monkeypatch):
+    spec = importlib.util.spec_from_file_location("_build_under_test", os.path.join(PKG, "build.py"))
+    b = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(b)
+    monkeypatch.setattr(b, "OBJ", str(tmp_path / "obj"))
+    monkeypatch.setattr(b, "LIB", str(tmp_path / "liblcp.so"))
+    monkeypatch.setattr(b, "BIND", str(tmp_path / "_serve.so"))
+    (tmp_path / "_serve.so").write_text("an older build")
+    flags = []
+
+    class Done:
+        returncode, stdout, stderr = 0, "", ""
+
+    class Failed(Done):
+        returncode, stderr = 1, "no such header"
+
+    def run(cmd, **kw):
+        if cmd[0] == "g++":
+            flags.extend(cmd)
+            return Failed
+        with open(cmd[cmd.index("-o") + 1], "w") as f:
+            f.write("built")
+        return Done
+
+    monkeypatch.setattr(b.subprocess, "run", run)
+    with pytest.raises(RuntimeError, match="bind.cpp"):
+        b.build()
+    assert (tmp_path / "liblcp.so").read_text() == "built"
+    assert not (tmp_path / "_serve.so").exists()         # not one of another version
+    import torch
+    assert "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch.compiled_with_cxx11_abi() in flags
