@@ -37,6 +37,22 @@ for call in (lambda: lcp.lcp_rope(x, x, x, i), lambda: lcp.PagedKVCache.empty(1,
     assert out.split() == ["told"] * 3
 
 
+def test_the_package_imports_where_torch_has_no_raw_stream():
+    """Those two names of torch are not public: without them the public ones serve."""
+    out = python('''
+import torch
+del torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+import learnable_channel_permutation_amd as lcp
+class S:
+    cuda_stream = 77
+torch.cuda.current_device = None
+torch.cuda.current_stream = lambda device=None: S
+lcp._lib._current_device = lambda: 0
+print(lcp._lib._stream(), lcp._lib._stream(S))
+''', ROOT)
+    assert out.split() == ["77", "77"]
+
+
 def test_the_library_is_built_where_the_serving_module_cannot_be(tmp_path, monkeypatch):
     spec = importlib.util.spec_from_file_location("_build_under_test", os.path.join(PKG, "build.py"))
     b = importlib.util.module_from_spec(spec)
