@@ -427,6 +427,8 @@ def lcp_kv_append(cache, k, v, slots, q=None, q_out=None, table=None, pos=None, 
 
 
 def lcp_kv_read(cache, slots, k_out, v_out, stream=None):
+    if k_out is None or v_out is None:
+        raise ValueError("k_out and v_out must be tensors")        # PagedKVCache.read makes them
     return _check("lcp_kv_read", _serve.read(cache, slots, k_out, v_out, stream)[0])
 
 

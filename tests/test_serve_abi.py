@@ -285,3 +285,14 @@ def test_every_public_name_exists():
     assert set(lcp.__all__) <= set(names)
     # the two that have no Python form of their own: messages come with LcpError, the version is the library's
     assert set(_lib().EXPORTS) - set(lcp.__all__) == {"lcp_status_string", "lcp_version"}
+
+
+def test_read_without_outputs_is_refused():
+    """They would be made, on the current stream whatever the call's is, and lost."""
+    import learnable_channel_permutation_amd as lcp
+    k, s = torch.zeros(4, 2, 16, 64, dtype=torch.int8), torch.zeros(4, 2, 16)
+    c, slots = lcp.PagedKVCache(k, k.clone(), s, s.clone()).c, torch.zeros(3, dtype=torch.int32)
+    out = torch.zeros(3, 2, 64)
+    for a in ((None, None), (out, None), (None, out)):
+        with pytest.raises(ValueError, match="k_out and v_out must be tensors"):
+            lcp.lcp_kv_read(c, slots, *a)
