@@ -462,7 +462,7 @@ int lcp_rope(const lcp_heads* q, const lcp_heads* k, lcp_dtype dt, int T, int D,
  *   E4M3: scale = the least power of two with a / scale <= 448, not under
  *         2^-126; code = x / scale rounded to e4m3 (nearest even).
  *   INT8: scale = max(a / 127, 2^-126); code = x / scale rounded to nearest
- *         even, held to [-127, 127].
+ *         even, held to [-127, 127]; both quotients are the nearest fp32 numbers.
  * A row with an infinity or a NaN is stored with a NaN scale, so that it reads
  * back as NaN and never as numbers that look right. */
 #define LCP_KV_BF16 0

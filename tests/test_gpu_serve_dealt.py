@@ -197,3 +197,12 @@ def test_append_writes_no_scale_but_its_own(fmt):
         for s, b in zip((c.k_scale, c.v_scale), before):
             s, b = (t.cpu().numpy().transpose(0, 2, 1) for t in (s, b))
             assert np.array_equal(s[rest], b[rest]) and not np.any(s[~rest] == b[~rest])
+
+
+@pytest.mark.parametrize("ps", [16, 80, 112, 496, 1008, 4080, 4096])
+def test_page_sizes(ps):
+    """Pages of any multiple of 16 tokens, cut and direct: the page of a tile and its place there."""
+    say("page sizes", ps)
+    assert_cut("int8", 3, 6, 2, 128, 9001)
+    check_attend("int8", [9001, 0, 4097], 6, 2, 128, ps)
+    check_attend("bf16", [490, 1, 479, 33], 6, 2, 128, ps, spare=1)
