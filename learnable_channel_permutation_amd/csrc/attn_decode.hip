@@ -85,30 +85,45 @@ struct Plan {
   float2* ml;            // [2 wgs][nh] maximum and sum
   int2* cuts;            // [B][units] place of the first piece, number of pieces
 };
-// Direct against dealt with its second kernel, us a pass: K of 128 KB (1 x 1000 fp8;
-// 16 x 1000; 64 x 1000) 10.2 / 10.0; 11.7 / 12.0; 20.0 / 22.5, 176 KB (x 1400) 12.5 /
-// 10.1; 14.6 / 13.0; 26.4 / 27.1, 256 KB (x 2000) 16.5 / 10.4; 19.4 / 14.4; 35.0 /
-// 33.0: up to 128 KB, and up to 192 where every compute unit has a unit. One takes in
-// about 50 KB a us, so that a direct workgroup of eight waves instead of four was
-// slower (1 x 1000: 10.9 us).
+// Direct against dealt with its second kernel, us a pass, fp8, 8 / 32 / 128 / 264 / 512
+// / 1024 units with K of half to all of: 96 KB 8.5 9.7 10.2 17.6 19.1 36.7 against 10.4
+// 11.0 13.4 17.6 25.2 41.1; 128 KB 10.1 11.2 12.1 21.7 23.8 44.8 against 10.1 10.9 13.8
+// 18.9 28.9 48.4; 160 KB 11.5 13.4 14.0 25.1 27.4 54.2 against 10.5 11.0 15.3 21.0 32.8
+// 56.8; 192 KB 13.0 15.1 16.1 29.2 32.1 63.3 against 10.9 11.2 16.0 23.0 36.9 65.2; 256
+// KB 16.9 18.8 20.1 37.5 41.3 81.7 against 11.0 11.4 17.8 27.9 45.0 81.7 (bf16 alike).
+// So direct up to 128 KB, and up to 192 where every compute unit has a unit, which loses
+// where a few units more than compute units make a second turn (264). A compute unit
+// takes in about 50 KB a us, so that a direct workgroup of eight waves instead of four
+// was slower (1 x 1000: 10.9 us).
 constexpr int kDirect = 128 << 10, kDirectMany = 192 << 10;
-// Cost of beginning and ending a unit, in steps: 5, 8, 12, 18 gave 42.0, 41.9, 42.5,
-// 44.5 us at 48 x 4096 fp8, 56.0, 54.8, 57.2, 59.0 at 128 x 1000 bf16 and 17.9, 16.0,
-// 16.7, 16.8 at 12 x 3000 of 256 int8 channels.
+// Cost of beginning and ending a unit, in steps: 4, 8, 12, 18 gave 47.4, 45.4, 45.8,
+// 47.2 us at 48 sequences of 1 to 4096, fp8; 56.9, 56.1, 58.1, 59.7 at 128 up to 1000,
+// bf16; 18.4, 16.6, 17.6, 17.4 at 12 up to 3000 of 256 int8 channels. Sequences of like
+// lengths (half of the largest at least) differ by 3 % between 8 and 12.
 constexpr int kExtra = 8;
 
 // How many parts the work is cut into, by its cost and the bytes of a step: parts of
 // 64 KB at least, and one a compute unit. A workgroup's four waves keep enough loads
 // in flight for it, and fewer streams reach more of the bandwidth; two workgroups a
 // unit pay only where conversions and unit ends, not the bytes, take the time: 8-bit
-// codes with 64 channels, or with 128 where the units are short.
+// codes with 64 channels, or with 128 where the units are many and short.
 // 256 / 512 / 768 parts, us: bf16 128 x 8192 323 / 334 / 341, 24 windows of 4096 (256
 // channels) 63.3 / 66.6 / -, 1 x 131071 87.2 / 90.9 / 93.9, 64 x 8000 (64 channels)
-// 85.7 / 88.7 / 90.2; 8-bit 2 x 131071 75.3 / 78.1 / 80.0, 20 x 8000 36.3 / 36.8 /
-// 38.4, but 48 x 4096 44.4 / 42.6 / 44.6, 64 x 2000 35.8 / 32.9 / 34.5 and with 64
-// channels 128 x 8192 128 / 98 / 101, 20 x 4096 18.3 / 16.1 / 17.8. Smaller work, with
-// 768 parts of 96 KB at least against this: 1 x 131071 of one head 24.4 / 19.3, 8 x
-// 3000 22.2 / 16.8, 1 x 40000 18.8 / 15.8.
+// 85.7 / 88.7 / 90.2; int8 2 x 131071 75.3 / 78.1 / 80.0. Smaller work, with 768 parts
+// of 96 KB at least against this: 1 x 131071 of one head 24.4 / 19.3, 8 x 3000 22.2 /
+// 16.8, 1 x 40000 18.8 / 15.8.
+// 256 / 512 parts of 8-bit codes, us (fp8; int8 is 2 % higher). 64 channels: 11 x 3000
+// 15.7 / 15.1, 30 x 3000 28.4 / 24.0, 5 x 8000 17.4 / 16.2, 64 x 8000 118 / 93, 4 x 30000
+// 32.4 / 27.9. 128 channels, 64 heads in 8 groups, lengths from 1 on, by the cost of the
+// work in thousands of steps: 8 (30 x 1600) 19.2 / 20.0, 9 (16 x 4096) 21.2 / 21.9, 14 (24
+// x 4096) 27.5 / 27.9, 14 (32 x 3000) 27.3 / 27.8, 16 (60 x 1600) 31.5 / 29.1, 21 (36 x
+// 4096) 37.0 / 36.3, 28 (64 x 3000) 47.3 / 44.7, 28 (48 x 4096) 46.1 / 43.9: from 12 on;
+// and by the mean cost of a unit: 39 (64 x 2000) 37.5 / 35.3, 55 (64 x 3000) 47.3 / 44.7,
+// 72 (96 x 4096) 80.0 / 79.6, 102 (32 x 6000) 42.9 / 43.4, 102 (64 x 6000) 78.1 / 76.8,
+// 133 (24 x 8000) 42.6 / 43.4, 258 (16 x 16000) 52.0 / 53.0: below 96. Sequences of like
+// lengths (half to one and a half of the mean) gain nothing: 36 x 1700 29.9 / 31.1, 50 x
+// 1700 39.6 / 40.0, 45 x 2000 39.8 / 40.6, 100 x 2500 94.5 / 96.0; the cut does not look
+// at how they differ.
 constexpr int most_parts(int E, int D) { return E == 1 && D <= 128 ? 512 : 256; }
 template <int E, int D>
 __device__ __forceinline__ uint32_t parts_of(uint32_t all, uint32_t units) {
@@ -683,8 +698,9 @@ hipError_t run(const AttnArgs& a, const Plan& p, hipStream_t s) {
   attn_units_kernel<FMT, D, HT, true><<<(unsigned)p.wgs, 256, 0, s>>>(a, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  // units against rows, us: 24 units 32.2 / 20.0 (24 x 8192, 32 heads), 64 units 37.3 /
-  // 33.5 (64 x 8192), 128 units 30.0 / 30.7 (128 x 4000, 16 heads), 256 units 47.9 / 49.8
+  // units against rows, us (bf16): 1 unit 58.5 / 24.4 (1 x 131071, 8 heads), 24 units 31.1 /
+  // 20.6 (24 x 8192, 32 heads), 64 units 37.3 / 35.9 (64 x 8192, 32 heads), 96 units 40.8 /
+  // 40.6 (96 x 8192, 16 heads), 128 units 30.3 / 31.1 (128 x 4000), 256 units 50.2 / 53.8
   if (units <= 64) {
     const int groups = p.units * p.nh;         // four pieces a unit and more, where the sequences are alike
     attn_join_kernel<D, true><<<(unsigned)(a.B * groups), 256, 0, s>>>(a, p, groups);

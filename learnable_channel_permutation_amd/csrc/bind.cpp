@@ -1,8 +1,8 @@
 // Marshalling of the serving calls: torch tensors -> the C ABI of include/lcp.h.
 // A decode step makes several calls of a few microseconds of GPU time; reading
 // tensors through Python attributes and ctypes took longer than the kernels
-// (us a call on the host, before -> here: lcp_rope 7.6 -> 3.8, append 8.1 -> 4.1,
-// attend with its outputs 10.2 -> 5.6). Shapes, types, layouts and devices are
+// (us a call on the host: lcp_rope 7.6, append 8.1, attend with its outputs 10.2; here
+// 4.2, 4.6 and 6.1, where a torch elementwise call takes 4.3). Shapes, types, layouts and devices are
 // checked here and raise ValueError or TypeError; everything else is the library's own
 // validation, whose status is returned.
 #include <Python.h>

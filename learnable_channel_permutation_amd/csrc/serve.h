@@ -61,9 +61,10 @@ __device__ __forceinline__ float rot_second(float a, float b, float c, float s) 
 // Loads and stores of data that nobody finds in the caches again: a call that
 // moves more than the 256 MB of the last-level cache hints them as streaming.
 // Measured on the rotary kernel (72 heads of 128 bf16) with a kernel that reads
-// its result, plain against hinted (us): 77 MB 27.4 / 29.5, 153 MB 51.1 / 51.9,
-// 306 MB 107.5 / 100.2, 612 MB 199.3 / 192.3; writing 16001 tokens into the
-// cache and reading 20097 back (655 + 494 MB) 237 / 208.
+// its result, plain against hinted (us): 75 MB 30.2 / 30.2, 150 MB 53.5 / 54.8,
+// 226 MB 79.6 / 77.5, 301 MB 106.7 / 99.8, 603 MB 197.7 / 191.9. Writing tokens into
+// an fp8 cache and reading them back, with nobody to read the result: 2000 (82 +
+// 49 MB) 32.4 / 29.0, 6000 82.3 / 74.0, 8000 (328 + 197 MB) 112 / 97, 16001 209 / 187.
 constexpr int64_t kStreamBytes = (int64_t)256 << 20;
 template <bool STREAM, typename T>
 __device__ __forceinline__ T load_as(const void* p) {
