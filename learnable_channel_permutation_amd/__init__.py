@@ -137,6 +137,8 @@ class PagedKVCache:
     sequence is the caller's: slots (page * page_size + offset) say where new
     tokens go, a page table [B, max_pages] and the lengths what a step reads.
     The tensors are the cache's for its life: k, v, k_scale and v_scale are read-only.
+    Calls run on the current stream, or on a given one: inputs have to be ready there, and
+    results are, in its order.
     """
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
@@ -177,9 +179,13 @@ class PagedKVCache:
         """Attention of one new token of each sequence, q [B, hq, D] bfloat16 (lcp_attn_decode): (out, lse). max_len,
         the host's bound on lens, defaults to what the page table can hold; scale to D^-1/2."""
         args = (self._c, q, pages, lens, max_len, out, lse, ws, scale, window, True)
-        if stream is None or (out is not None and lse is not None and ws is not None):
-            code, out, lse = _lib._serve.attend(*args, stream)
-        else:
+        made = stream is not None and (out is None or lse is None)
+        if stream is not None and not made and ws is None:
+            n = pages.shape[1] * self._c.page_size if max_len is None else max_len
+            made = lcp_attn_decode_workspace_bytes(self._c, q.shape[0], q.shape[1], n, window) > 0
+        if made:
             code, out, lse = _made_on(stream, (out, lse), _lib._serve.attend, *args)
+        else:
+            code, out, lse = _lib._serve.attend(*args, stream)
         _lib._check("lcp_attn_decode", code)
         return out, lse

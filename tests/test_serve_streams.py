@@ -75,3 +75,22 @@ def test_allocations_belong_to_the_stream_that_uses_them(call, monkeypatch):
     assert watched.seen and all(x is side for x in watched.seen)
     # results that were made are used by the caller's stream next: kept until it is done with them
     assert kept == ["caller's"] * {"read": 2, "read one": 1, "attend": 2, "attend workspace": 0}[call]
+
+
+@pytest.mark.parametrize("max_len", [None, 64])
+def test_a_call_that_makes_nothing_passes_its_stream_on(max_len, monkeypatch):
+    """Outputs given and no workspace needed: no change of the current stream, which costs more than the call."""
+    class Handle:
+        cuda_stream = 7
+
+    got = []
+    monkeypatch.setattr(torch.cuda, "stream", lambda stream: pytest.fail("the current stream was changed"))
+    monkeypatch.setattr(Native, "attend", staticmethod(lambda *a: (got.append(a[-1]), (0, a[5], a[6]))[1]))
+    monkeypatch.setattr(lcp._lib, "_serve", Native)
+    cache = lcp.PagedKVCache.__new__(lcp.PagedKVCache)
+    cache._c = lcp._lib.lcp_kv_cache(4096, 8192, 4096, 4096, lcp._lib.LCP_KV_INT8, 4, 16, 2, 64)
+    q, h = torch.zeros(3, 4, 64, dtype=torch.bfloat16), Handle()
+    out, lse = torch.zeros_like(q), torch.zeros(3, 4)
+    assert cache.attend(q, torch.zeros(3, 4, dtype=torch.int32), torch.zeros(3, dtype=torch.int32), max_len=max_len, out=out,
+                        lse=lse, stream=h)[0] is out
+    assert got == [h]
