@@ -611,6 +611,8 @@ typedef struct lcp_packed {
   const float*    wscale;    /* [cout], E4M3 only (else NULL)                  */
   lcp_dtype       dt;        /* BF16 (lcp_sparse_pack) or E4M3                 */
   int             cout, cin; /* cout % 32 == 0, cin % 32 == 0                  */
+  int             fast;      /* 0, or E4M3 only: 1, sums of fewer bits allowed
+                                (lcp_sparse_linear)                            */
 } lcp_packed;
 
 /* Activations (lcp_epilogue.act). */
@@ -639,9 +641,10 @@ typedef struct lcp_epilogue {
  * is in its permuted channel order (lcp_rms_norm's perm, lcp_gather_channels);
  * a product that feeds another deployed layer can have that layer's order packed
  * into its rows. e may be NULL. Equal calls give equal bits; another T may cut the
- * sums elsewhere. E4M3 with bf16 outputs and more than 64 tokens: the matrix
- * instruction adds sixteen products with the bits below 2^-13 of the largest
- * dropped; otherwise products are exact and sums fp32.
+ * sums elsewhere. Products are exact and sums fp32. An E4M3 layer that is `fast`
+ * lets bf16 outputs of more than 64 tokens come from the e4m3 matrix instruction,
+ * which adds sixteen products with the bits below 2^-13 of the largest dropped: a
+ * sum far smaller than its terms may then be all error.
  *   x, gate, y and residual rows 16-byte aligned (pointers and strides); bias
  *   and wscale 16-byte, x_scale 4-byte aligned. (T - 1) x_row + cin < 2^31
  *   bytes' worth of elements; cout * cin < 2^31 (bf16: 2^30). A position that

@@ -108,7 +108,7 @@ class lcp_norm(ctypes.Structure):
 
 class lcp_packed(ctypes.Structure):
     _fields_ = [("vals", ctypes.c_void_p), ("meta", ctypes.c_void_p), ("wscale", ctypes.c_void_p),
-                ("dt", ctypes.c_int), ("cout", ctypes.c_int), ("cin", ctypes.c_int)]
+                ("dt", ctypes.c_int), ("cout", ctypes.c_int), ("cin", ctypes.c_int), ("fast", ctypes.c_int)]
     gpu = -2                # as in lcp_kv_cache
     tensors = None
 
@@ -511,9 +511,13 @@ def lcp_sparse_pack_e4m3(W, B, perm, bits, vals, meta, wscale, stream=None):
                                                                    _p(meta), _p(wscale), _stream(stream)))
 
 
-def make_packed(vals, meta, cout, cin, wscale=None):
-    """lcp_packed over the outputs of lcp_sparse_pack, or with wscale of lcp_sparse_pack_e4m3."""
+def make_packed(vals, meta, cout, cin, wscale=None, fast=False):
+    """lcp_packed over the outputs of lcp_sparse_pack, or with wscale of lcp_sparse_pack_e4m3 (fast: sums of fewer bits
+    allowed, as lcp_sparse_linear says)."""
+    if fast and wscale is None:
+        raise ValueError("fast belongs to 8-bit layers")
     p = lcp_packed.from_buffer_copy(_serve.packed(vals, meta, wscale, cout, cin))
+    p.fast = bool(fast)
     p.gpu = vals.get_device()
     p.tensors = (vals, meta, wscale)
     return p

@@ -53,7 +53,7 @@ struct PackedArgs {
   const u32x4* vals;
   const uint32_t* meta;
   const float* wscale;
-  int fp8, cout, cin;
+  int fp8, cout, cin, fast;
 };
 size_t sparse_vals_bytes_e4m3(int cout, int cin);
 size_t sparse_meta_bytes_e4m3(int cout, int cin);

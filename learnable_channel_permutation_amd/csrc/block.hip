@@ -44,10 +44,11 @@ int check_packed(const lcp_packed* w, PackedArgs* out) {
   if (rc != LCP_OK) return rc;
   if (!w->vals || !w->meta || !aligned(w->vals, 16) || !aligned(w->meta, 4)) return LCP_E_INVAL;
   const bool fp8 = w->dt == LCP_E4M3;
+  if (w->fast != 0 && (w->fast != 1 || !fp8)) return LCP_E_INVAL;
   if (fp8 && (!w->wscale || !aligned(w->wscale, 16))) return LCP_E_INVAL;
   // the weights are read through 32-bit byte offsets
   if ((int64_t)w->cout * w->cin >= ((int64_t)1 << (fp8 ? 31 : 30))) return LCP_E_INVAL;
-  *out = PackedArgs{(const u32x4*)w->vals, w->meta, fp8 ? w->wscale : nullptr, fp8, w->cout, w->cin};
+  *out = PackedArgs{(const u32x4*)w->vals, w->meta, fp8 ? w->wscale : nullptr, fp8, w->cout, w->cin, w->fast};
   return LCP_OK;
 }
 

@@ -562,12 +562,13 @@ size_t sparse_linear_workspace_bytes(const PackedArgs& w, int T) {
   return (size_t)((most + 255) / 256 * 256);
 }
 
-// e4m3: exact products where fp32 comes out, and for few tokens, where they cost nothing
-// (us, converted against e4m3 instructions: 64 tokens of 4096 <- 4096 5.8 / 5.5, 128 8.6 / 7.6;
-// 4096 tokens of 28672 <- 8192 747 / 541).
+// e4m3: exact products, but where the layer's user asked for the e4m3 instructions, whose dropped bits are the whole
+// result where sums cancel; not for fp32 outputs, nor for few tokens, where exact products cost nothing (us,
+// converted against e4m3 instructions: 64 tokens of 4096 <- 4096 5.8 / 5.5, 128 8.6 / 7.6; 4096 tokens of
+// 28672 <- 8192 747 / 541).
 hipError_t launch_sparse_linear(const LinearArgs& a, hipStream_t s) {
   if (!a.w.fp8) return run_linear<M_BF16>(a, s);
-  if (a.e.y_f32 || a.T < kTilesFrom) return run_linear<M_E4M3>(a, s);
+  if (!a.w.fast || a.e.y_f32 || a.T < kTilesFrom) return run_linear<M_E4M3>(a, s);
   return run_linear<M_E4M3_FAST>(a, s);
 }
 

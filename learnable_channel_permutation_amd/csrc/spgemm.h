@@ -17,8 +17,9 @@ typedef __attribute__((address_space(3))) void* dep_lds_t;
 
 // How a product's operands are multiplied. The e4m3 instructions add the products of
 // one lane (sixteen) with bits below 2^-13 of the largest dropped, 1.5e-5 of a sum's
-// size (measured; the dense and the scaled ones alike): nothing beside a bf16 output's
-// 2^-9, too much for an fp32 one. M_E4M3 turns the codes into bf16 instead, exactly.
+// size (measured; the dense and the scaled ones alike): less than a bf16 output's 2^-9 of
+// a sum as large as its terms, but all of one whose terms cancel (224 terms of size 1 beside
+// 16 pairs of +-2^14: 0 for 224). M_E4M3 turns the codes into bf16 instead, exactly.
 enum SparseMode { M_BF16 = 0, M_E4M3 = 1, M_E4M3_FAST = 2 };
 
 __device__ __forceinline__ u32x8 cat(u32x4 a, u32x4 b) {

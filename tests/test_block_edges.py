@@ -1,0 +1,29 @@
+"""What a decoder block's operators refuse at the edges of what their documents allow, without a GPU."""
+import ctypes
+
+import pytest
+import torch
+
+import learnable_channel_permutation_amd as lcp
+from learnable_channel_permutation_amd import _lib as L
+
+P = 0x100000
+
+
+def test_fast_belongs_to_8_bit_layers():
+    n = ctypes.c_size_t(0)
+    for dt, fast, want in ((L.LCP_E4M3, 0, L.LCP_OK), (L.LCP_E4M3, 1, L.LCP_OK), (L.LCP_BF16, 0, L.LCP_OK),
+                           (L.LCP_BF16, 1, L.LCP_E_INVAL), (L.LCP_E4M3, 2, L.LCP_E_INVAL), (L.LCP_E4M3, -1, L.LCP_E_INVAL)):
+        p = L.lcp_packed(P, 2 * P, 3 * P, dt, 64, 128, fast)
+        assert L.LIB.lcp_sparse_linear_workspace_bytes(ctypes.byref(p), 80, ctypes.byref(n)) == want, (dt, fast)
+    assert ctypes.sizeof(L.lcp_packed) == 40
+    vb, mb = lcp.lcp_sparse_pack_bytes(96, 64)
+    bf = torch.zeros(vb, dtype=torch.uint8), torch.zeros(mb // 4, dtype=torch.int32)
+    assert lcp.SparseLinear(*bf, 96, 64).fast is False
+    vb, mb = lcp.lcp_sparse_pack_e4m3_bytes(96, 64)
+    f8 = torch.zeros(vb, dtype=torch.uint8), torch.zeros(mb // 4, dtype=torch.int32)
+    assert lcp.SparseLinear(*f8, 96, 64, torch.ones(96)).fast is False
+    assert lcp.SparseLinear(*f8, 96, 64, torch.ones(96), fast=True).fast is True
+    for bad in (lambda: lcp.SparseLinear(*bf, 96, 64, fast=True), lambda: lcp.make_packed(*bf, 96, 64, None, True)):
+        with pytest.raises(ValueError):
+            bad()
