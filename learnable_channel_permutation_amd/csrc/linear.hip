@@ -58,7 +58,9 @@ __device__ __forceinline__ void activate(f32x4* v, int act) {
 __device__ __forceinline__ f32x4 pairs(u32x2 w) { return f32x4{lo_bf(w[0]), hi_bf(w[0]), lo_bf(w[1]), hi_bf(w[1])}; }
 
 // The epilogue for R rows of a token (4, or 8 with a wave on whole lines): what it reads
-// by row alone, what it reads by token, and the rest.
+// by row alone, what it reads by token, and the rest. A row's and a token's scale may each be
+// 2^120 or 2^-126, and their product past fp32 where the scaled sum is not: their fractions
+// are multiplied (exactly, for powers of two) and their exponents added.
 template <int R>
 struct Finish {
   static constexpr int kRows = R, Q = R / 4;
@@ -66,7 +68,8 @@ struct Finish {
   typedef uint32_t Words __attribute__((ext_vector_type(R / 2)));      // R bf16 numbers
   Epilogue e;
   struct Fixed {
-    f32x4 scale[Q];
+    f32x4 scale[Q];                            // fractions
+    i32x4 power[Q];
     Words bias;
   };
   struct Loaded {
@@ -78,7 +81,14 @@ struct Finish {
     Fixed f;
     if (e.wscale) {
 #pragma unroll
-      for (int i = 0; i < Q; ++i) f.scale[i] = *(const f32x4*)(e.wscale + o + 4 * i);
+      for (int i = 0; i < Q; ++i) {
+        const f32x4 s = *(const f32x4*)(e.wscale + o + 4 * i);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          f.scale[i][j] = __builtin_amdgcn_frexp_mantf(s[j]);
+          f.power[i][j] = __builtin_amdgcn_frexp_expf(s[j]);
+        }
+      }
     }
     if (e.bias) f.bias = *(const Words*)(e.bias + o);
     return f;
@@ -101,8 +111,13 @@ struct Finish {
   }
   __device__ __forceinline__ void finish(int64_t t, int o, f32x4* v, const Fixed& f, const Loaded& l) const {
     if (e.wscale) {
+      const float fraction = __builtin_amdgcn_frexp_mantf(l.xscale);
+      const int power = __builtin_amdgcn_frexp_expf(l.xscale);
 #pragma unroll
-      for (int i = 0; i < Q; ++i) v[i] *= f.scale[i] * l.xscale;
+      for (int i = 0; i < Q; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          v[i][j] = __builtin_ldexpf(v[i][j] * (f.scale[i][j] * fraction), f.power[i][j] + power);
     }
     if (e.bias) {
 #pragma unroll

@@ -65,3 +65,45 @@ def test_fast_layers(T):
         top = [t.double().abs().view(len(t), -1, 32).amax(-1) for t in (x.float(), eye)]
         tol = 16 * 2.0 ** -13 * (top[0] @ top[1].T) + 2 * (256 + 64) * 2.0 ** -24 * (x.double().abs() @ eye.abs().T)
         assert bool(((y - z).abs() <= tol + 2.0 ** -8 * (z.abs() + tol)).all())
+
+
+@pytest.mark.parametrize("T,yt", [(1, F32), (1, BF), (40, F32), (70, BF), (70, F32), (300, BF), (300, F32), (2000, BF)])
+def test_scales_whose_product_passes_fp32(T, yt):
+    """A row's scale 2^110 and tokens' of 2^30 and 2^-126: sums of 0 and of 2^-18 (the smallest codes' product). And
+    2^-126 for both, where nothing is left of a sum."""
+    say("scales", T, yt)
+    W = torch.zeros(64, 512, device=DEV)
+    W[:, 0], W[:, 1] = 1.75 * 2.0 ** 118, 2.0 ** 101
+    W[32:] *= 2.0 ** -118                                # their scale: 2^-8
+    lin = straight(W, F8)
+    assert bool((lin.scale[:32] == 2.0 ** 110).all()) and bool((lin.scale[32:] == 2.0 ** -8).all())
+    x, s = torch.zeros(T, 512, device=DEV), torch.full((T,), 2.0 ** 30, device=DEV)
+    x[::2, 1] = 2.0 ** -9                                # W's code there is 2^-9, too
+    s[4::4] = 2.0 ** -126
+    y = lin(x.to(F8), scale=s, dtype=yt)
+    want = torch.where(x[:, 1:2] > 0, 2.0 ** -18 * s[:, None], torch.zeros((), device=DEV)).expand(T, 64).double()
+    want = want * lin.scale.double()
+    want[:, 32:][s == 2.0 ** -126] = 0                   # 2^-18 2^-126 2^-8: nothing of it in fp32
+    assert bool(torch.isfinite(want).all()) and float(want.max()) == 2.0 ** 122
+    assert torch.equal(y.double(), want)
+    lin = straight(torch.zeros(64, 512, device=DEV), F8)
+    y = lin(torch.full((T, 512), 448.0, device=DEV).to(F8), scale=torch.full((T,), 2.0 ** -126, device=DEV), dtype=yt)
+    assert bool((y == 0).all())
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), 0.0])
+@pytest.mark.parametrize("T", [3, 70, 300])
+def test_token_scales_that_are_no_powers_of_two(T, bad):
+    """Any number is a scale: the product of two fractions is rounded once, and NaN, infinity and 0 are what they are."""
+    g = torch.Generator(device=DEV).manual_seed(T)
+    lin = straight(torch.randn(64, 96, generator=g, device=DEV), F8)
+    x = torch.randn(T, 96, generator=g, device=DEV).to(F8)
+    s = torch.rand(T, generator=g, device=DEV) + 0.3
+    one = lin(x, scale=torch.ones(T, device=DEV), dtype=F32)
+    y = lin(x, scale=s, dtype=F32).double()
+    want = one.double() * s.double()[:, None]
+    assert bool(((y - want).abs() <= 2.0 ** -24 * 1.01 * 2 * want.abs()).all())      # the fractions' product and the sum's
+    s[T // 2] = bad
+    z = lin(x, scale=s, dtype=F32)[T // 2]
+    row = one[T // 2] * bad
+    assert torch.equal(z.isnan(), row.isnan()) and torch.equal(z[~row.isnan()], row[~row.isnan()])
