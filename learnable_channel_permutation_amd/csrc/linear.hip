@@ -16,24 +16,69 @@ namespace {
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-// 1 / (1 + exp(-v)), by the hardware's exponential and reciprocal (each good to one
-// unit in the last place; the library's take ten times as long, as long as a tile's
-// whole product: 256 x 128 values in 12 us).
-__device__ __forceinline__ float sigmoid(float v) {
-  return __builtin_amdgcn_rcpf(1.f + exp2_(-1.4426950408889634f * v));
+// Exponentials and reciprocals are the hardware's, each good to one unit in the last place (the library's take
+// ten times as long, as long as a tile's whole product: 256 x 128 values in 12 us). Where bf16 comes out an
+// exponent is rounded as it is formed: off by 2^-15 at most. Where fp32 comes out what it loses is a second
+// number, and all of an activation is good to 12 roundings, relative to its value.
+// 2^(hi + lo), lo small beside 1.
+__device__ __forceinline__ float exp2_sum(float hi, float lo) {
+  const float e = exp2_(hi);
+  return fmaf(0.693147181f * e, lo, e);
 }
-// erfc(z) for z >= 0, off by 1.5e-7 at most: Abramowitz and Stegun, Handbook of
-// Mathematical Functions, 7.1.26.
-__device__ __forceinline__ float erfc_(float z) {
-  const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, z, 1.f));
-  float p = fmaf(1.061405429f, t, -1.453152027f);
-  p = fmaf(p, t, 1.421413741f);
-  p = fmaf(p, t, -0.284496736f);
-  p = fmaf(p, t, 0.254829592f);
-  return p * t * exp2_(-1.4426950408889634f * z * z);
+// log2 e and what fp32 drops of it.
+constexpr float kLog2e = 1.4426950216293335f, kLog2eLow = 1.925963033500011e-08f;
+// 1 / (1 + exp(-v)).
+__device__ __forceinline__ float sigmoid(float v) {
+  return __builtin_amdgcn_rcpf(1.f + exp2_(-kLog2e * v));
+}
+// The same from e = exp(-|v|).
+__device__ __forceinline__ float sigmoid_of(float v, float e) {
+  return (v < 0.f ? e : 1.f) * __builtin_amdgcn_rcpf(1.f + e);
+}
+template <bool FP32>
+__device__ __forceinline__ float silu(float v) {
+  if constexpr (!FP32) return v * sigmoid(v);
+  const float x = fminf(fabsf(v), 128.f), hi = -kLog2e * x;             // exp(-128) is 0
+  return v * sigmoid_of(v, exp2_sum(hi, fmaf(-kLog2eLow, x, fmaf(-kLog2e, x, -hi))));
+}
+// v (1 + erf(v / sqrt 2)) / 2 = v erfc(z) / 2 for v < 0 and v (1 - erfc(z) / 2) else, z = |v| / sqrt 2. erfc(z) / 2 is
+// t P(t) exp(-z^2) with t = 1 / (1 + 3 z / 8): P of degree 8 fitted to the smallest relative error on z <= 11 (beyond,
+// exp(-z^2) is 0), 2^-25.7. An erfc that is good to 1.5e-7 absolute alone leaves 2 % of the values between v = -10 and -4.
+template <bool FP32>
+__device__ __forceinline__ float gelu(float v) {
+  const float x = fminf(fabsf(v), 16.f), a = x * x, hi = -0.5f * kLog2e * a;
+  float e;
+  if constexpr (FP32) {
+    const float low = fmaf(x, x, -a);
+    e = exp2_sum(hi, fmaf(-0.5f * kLog2e, low, fmaf(-0.5f * kLog2eLow, a, fmaf(-0.5f * kLog2e, a, -hi))));
+  } else {
+    e = exp2_(hi);
+  }
+  const float t = __builtin_amdgcn_rcpf(fmaf(0.2651650309562683f, x, 1.f));
+  float p = fmaf(0.03024500422179699f, t, -0.14119213819503784f);
+  p = fmaf(p, t, 0.21124452352523804f);
+  p = fmaf(p, t, -0.10921130329370499f);
+  p = fmaf(p, t, 0.1331809163093567f);
+  p = fmaf(p, t, 0.062274374067783356f);
+  p = fmaf(p, t, 0.10227838158607483f);
+  p = fmaf(p, t, 0.1053764596581459f);
+  p = fmaf(p, t, 0.10580378025770187f);
+  const float tail = p * t * e;
+  return v * (v < 0.f ? tail : 1.f - tail);
+}
+// 1 + tanh(u) = 2 / (1 + exp(-2u)), 2 u = 2 sqrt(2 / pi) v (1 + 0.044715 v^2).
+template <bool FP32>
+__device__ __forceinline__ float gelu_tanh(float v) {
+  if constexpr (!FP32) return v * sigmoid(1.5957691216057308f * fmaf(0.044715f * v * v, v, v));
+  constexpr float K = 0.044714998453855515f, KLOW = 1.5461444347053543e-09f;
+  constexpr float C = 2.302208185195923f, CLOW = 1.2948402350332344e-08f;      // 2 sqrt(2 / pi) log2 e
+  const float x = fminf(fabsf(v), 16.f), a = x * x;                            // exp(-2u) is 0 from there on
+  const float q = fmaf(K, a, 1.f), qlow = fmaf(K, fmaf(x, x, -a), fmaf(KLOW, a, fmaf(K, a, 1.f - q)));
+  const float m = x * q, mlow = fmaf(x, qlow, fmaf(x, q, -m)), hi = -C * m;
+  return v * sigmoid_of(v, exp2_sum(hi, fmaf(-C, mlow, fmaf(-CLOW, m, fmaf(-C, m, -hi)))));
 }
 // The activation of N values; the branch on which one is taken once for all of them.
-template <int N>
+template <int N, bool FP32>
 __device__ __forceinline__ void activate(f32x4* v, int act) {
   const auto each = [&](auto f) {
 #pragma unroll
@@ -41,16 +86,9 @@ __device__ __forceinline__ void activate(f32x4* v, int act) {
   };
   switch (act) {
     case 1: each([](float v) { return v < 0.f ? 0.f : v; }); break;
-    case 2: each([](float v) { return v * sigmoid(v); }); break;
-    case 3:
-      each([](float v) {
-        const float c = 0.5f * erfc_(fabsf(v) * 0.70710678118654752f);
-        return v * (v < 0.f ? c : 1.f - c);
-      });
-      break;
-    case 4:                                    // 1 + tanh(u) = 2 / (1 + exp(-2u))
-      each([](float v) { return v * sigmoid(1.5957691216057308f * fmaf(0.044715f * v * v, v, v)); });
-      break;
+    case 2: each([](float v) { return silu<FP32>(v); }); break;
+    case 3: each([](float v) { return gelu<FP32>(v); }); break;
+    case 4: each([](float v) { return gelu_tanh<FP32>(v); }); break;
     default: break;
   }
 }
@@ -123,7 +161,8 @@ struct Finish {
 #pragma unroll
       for (int i = 0; i < Q; ++i) v[i] += pairs(u32x2{f.bias[2 * i], f.bias[2 * i + 1]});
     }
-    activate<R>(v, e.act);
+    if (e.y_f32) activate<R, true>(v, e.act);
+    else activate<R, false>(v, e.act);
     if (e.gate) {
 #pragma unroll
       for (int i = 0; i < Q; ++i) v[i] *= pairs(u32x2{l.gate[2 * i], l.gate[2 * i + 1]});

@@ -1,9 +1,12 @@
 """Values and calls at the edges of what the documents of a decoder block's operators allow (root-mean-square norm, its
 gradient, the 2:4 product with an epilogue), against their 64-bit definitions."""
+import math
+
+import numpy as np
 import pytest
 import torch
 
-from tests.gpu_util import DEV, say
+from tests.gpu_util import DEV, down, say
 
 pytestmark = pytest.mark.gpu
 
@@ -107,3 +110,36 @@ def test_token_scales_that_are_no_powers_of_two(T, bad):
     z = lin(x, scale=s, dtype=F32)[T // 2]
     row = one[T // 2] * bad
     assert torch.equal(z.isnan(), row.isnan()) and torch.equal(z[~row.isnan()], row[~row.isnan()])
+
+
+@pytest.mark.parametrize("yt", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+def test_activations_relative_to_their_values(act, yt):
+    """From -86 to 40, tails and all. fp32: one unit in the last place (two roundings) each of the exponential and the
+    reciprocal, one of its correction, at most three of a polynomial of fitted error 0.3 * 2^-24 and three products: 12.
+    bf16: 2^-15 of an exponent that is rounded, and the output's rounding."""
+    say("activation", act, yt)
+    T = 2048
+    g = torch.Generator().manual_seed(7)
+    v = torch.cat([torch.linspace(-86, 40, T * 3), torch.linspace(-14, 14, T * 4), 0.01 * torch.randn(T, generator=g)])
+    hi = v.view(8, T).T.to(BF)
+    lo = (v.view(8, T).T - hi.float()).to(BF)            # two products that are added exactly: 16 bits of v
+    x, W = torch.zeros(T, 32, dtype=BF), torch.zeros(32, 32)
+    x[:, 0::4], x[:, 1::4] = hi, lo
+    for i in range(8):
+        W[i, 4 * i:4 * i + 2] = 1
+    z = hi.double().numpy() + lo.double().numpy()
+    if act == "silu":
+        ref = np.where(z < 0, z * np.exp(z) / (1 + np.exp(z)), z / (1 + np.exp(-np.abs(z))))
+    elif act == "gelu":
+        ref = 0.5 * z * np.vectorize(math.erfc)(-z / math.sqrt(2))
+    else:
+        u = 2 * math.sqrt(2 / math.pi) * (z + 0.044715 * z ** 3)
+        ref = np.where(z < 0, z * np.exp(np.minimum(u, 0)) / (1 + np.exp(np.minimum(u, 0))), z / (1 + np.exp(-np.abs(u))))
+    tol = 12 * 2.0 ** -24 if yt == F32 else 2.0 ** -15 * (1 + 2.0 ** -8) + 2.0 ** -8
+    lin = straight(W.to(DEV), BF)
+    for n in (1, 40, T):
+        rows = torch.arange(0, T, max(1, T // n))[:n]
+        y = down(lin(x[rows].to(DEV), act=act, dtype=yt))[:, :8]
+        r = ref[rows.numpy()]
+        assert np.all(np.abs(y - r) <= tol * np.abs(r) + 2.0 ** -118)
