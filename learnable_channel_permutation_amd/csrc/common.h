@@ -136,6 +136,13 @@ __device__ __forceinline__ float e4m3_scale(uint32_t a) {
 }
 
 // ---- wave helpers -------------------------------------------------------------
+// Between what lanes of a wave write to LDS and what others of it read there, and back:
+// a wave's LDS instructions are carried out in order; the compiler has to keep them so.
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
 __device__ __forceinline__ float shfl_xor(float v, int mask) { return __shfl_xor(v, mask, 64); }
 
 // Lane moves inside a row of 16 lanes (DPP): CTRL 0xB1 / 0x4E swap lanes at

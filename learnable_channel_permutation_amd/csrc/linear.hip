@@ -334,6 +334,7 @@ __global__ __launch_bounds__(64 * W) void linear_thin_kernel(LinearArgs a, uint3
     for (int i = 0; i < RT; ++i) { cw[i] = w[i]; ci[i] = E == 1 ? idx[i] : idx[i] >> (16 * (g >> 1)); }
 #pragma unroll
     for (int j = 0; j < X; ++j) mine[64 * j + (put ^ (4 * (j & 1)))] = v[j];
+    wave_fence();
     s += W;
     if (s < KS) load(s);
 #pragma unroll
@@ -343,6 +344,7 @@ __global__ __launch_bounds__(64 * W) void linear_thin_kernel(LinearArgs a, uint3
 #pragma unroll
       for (int i = 0; i < RT; ++i) acc[i][j] = smfma16<MODE>(Wgt16<MODE>(cw[i], ci[i]), b, acc[i][j]);
     }
+    wave_fence();
   }
   // a round of tiles: every wave's sums to LDS, then added in the waves' order
   f32x4* const sums = (f32x4*)lds;

@@ -169,12 +169,6 @@ __device__ __forceinline__ void in_order(const unsigned char* lds, const uint32_
     w[(j + 1) / K] |= (uint32_t)((const E_*)lds)[two >> 16] << (8 * sizeof(E) * ((j + 1) % K));
   }
 }
-// A wave's LDS instructions are carried out in order; the compiler has to keep them so.
-__device__ __forceinline__ void wave_fence() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
 
 // V weights from c on as fp32.
 template <int V>

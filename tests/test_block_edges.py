@@ -1,5 +1,7 @@
 """What a decoder block's operators refuse at the edges of what their documents allow, without a GPU."""
 import ctypes
+import os
+import re
 
 import pytest
 import torch
@@ -27,3 +29,24 @@ def test_fast_belongs_to_8_bit_layers():
     for bad in (lambda: lcp.SparseLinear(*bf, 96, 64, fast=True), lambda: lcp.make_packed(*bf, 96, 64, None, True)):
         with pytest.raises(ValueError):
             bad()
+
+
+def _kernel(file, name):
+    """The source of a kernel, from its name to the end of its body."""
+    path = os.path.join(os.path.dirname(os.path.abspath(lcp.__file__)), "csrc", file)
+    text = open(path).read()
+    at = text.index(name + "(")
+    return text[at:text.index("\n}\n", at)]
+
+
+def test_lanes_that_exchange_through_lds_are_fenced():
+    """What a lane reads of a wave's LDS may come from another lane: no run shows a compiler that swaps the two, so the
+    fences between writes and reads, and between reads and the next step's writes, are held in the source."""
+    body = _kernel("linear.hip", "linear_thin_kernel")
+    loop = body[body.index("while (s < KS) {"):body.index("// a round of tiles")]
+    events = [m.group(0) for m in re.finditer(r"mine\[[^;]*\] = |wave_fence\(\)|mine\[n", loop)]
+    kinds = ["write" if " = " in e else "fence" if "fence" in e else "read" for e in events]
+    assert kinds == ["write", "fence", "read", "read", "fence"], events
+    body = _kernel("norm.hip", "norm_kernel")
+    kinds = re.findall(r"to_order<|wave_fence\(\)|in_order<", body)
+    assert kinds == ["to_order<", "wave_fence()", "in_order<", "wave_fence()"]
