@@ -8,6 +8,8 @@
 // NT threads with NV chunks of 16 bytes each, in registers from the loads to the
 // stores, so that every input is read once; the next row's loads fly during this
 // one's sums. The weight (and the gather's places) are loaded once a workgroup.
+#include <type_traits>
+
 #include "block.h"
 
 namespace lcp {
@@ -222,8 +224,9 @@ __device__ __forceinline__ float sum_of(const float* p) {
 
 // The factor s from a row's sum of squares. Where that passed fp32's range, h is
 // scaled by kSmall first: the sum then has a square of 1e17 2^-96 or more, of 2^64 at
-// most, and eps is nothing beside it.
-constexpr float kSmall = 0x1p-96f;
+// most, and eps is nothing beside it. Half of the scaling (its root) then meets h and half the
+// factor, so that nothing becomes subnormal on the way which is not in the end.
+constexpr float kSmall = 0x1p-96f, kSmallRoot = 0x1p-48f;
 __device__ __forceinline__ float factor(float ss, int C, float eps) { return 1.f / sqrtf(ss / (float)C + eps); }
 
 // What the registers hold besides a thread's elements (1024 threads leave 128 of them):
@@ -303,7 +306,7 @@ __global__ __launch_bounds__(NT) void norm_kernel(NormArgs a) {
       __syncthreads();
       return sum_of<W>(part[turn]);
     };
-    float ss = squares(1.f), by = 1.f, s = factor(ss, a.C, a.eps);
+    float ss = squares(1.f), s = factor(ss, a.C, a.eps);
     if (a.sum.p) {
       void* sum = row_at(a.sum, t, sizeof(XT));
 #pragma unroll
@@ -314,8 +317,11 @@ __global__ __launch_bounds__(NT) void norm_kernel(NormArgs a) {
     }
     if (!(ss < __builtin_inff())) {            // the same for the whole workgroup
       __syncthreads();
-      by = kSmall;
-      s = factor(squares(by), a.C, 0.f);
+      s = factor(squares(kSmall), a.C, 0.f) * kSmallRoot;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) h[i][j] *= kSmallRoot;
     }
     uint32_t top = 0;
 #pragma unroll
@@ -326,7 +332,7 @@ __global__ __launch_bounds__(NT) void norm_kernel(NormArgs a) {
       }
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        h[i][j] = h[i][j] * by * s * w[HELD ? i : 0][j];
+        h[i][j] = h[i][j] * s * w[HELD ? i : 0][j];
         top = max(top, __float_as_uint(h[i][j]) & 0x7fffffffu);
       }
     }
@@ -442,9 +448,9 @@ __global__ __launch_bounds__(NT) void norm_grad_kernel(NormGradArgs a) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) { ch[i] = nh[i]; cy[i] = ny[i]; cs[i] = ns[i]; }
     if (AHEAD && t + gridDim.x < a.T) load(t + gridDim.x);
-    float by = 1.f, s, gn;
-    for (;;) {                                 // once, or twice where the squares pass fp32's range
-      float ss = 0.f, gh = 0.f;
+    float root = 1.f, ss, gh;
+    auto sums = [&](auto scaled) {             // of squares, and of g (h root)
+      ss = gh = 0.f;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         float h[V], dy[V];
@@ -456,8 +462,8 @@ __global__ __launch_bounds__(NT) void norm_grad_kernel(NormGradArgs a) {
         }
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          const float v = h[j] * by;
-          ss = fmaf(v, v, ss);
+          const float v = scaled ? h[j] * root : h[j], u = scaled ? v * root : v;
+          ss = fmaf(u, u, ss);
           gh = fmaf(dy[j] * w[HELD ? i : 0][j], v, gh);
         }
       }
@@ -467,12 +473,16 @@ __global__ __launch_bounds__(NT) void norm_grad_kernel(NormGradArgs a) {
       __syncthreads();
       ss = sum_of<W>(part[turn][0]);
       gh = sum_of<W>(part[turn][1]);
-      s = factor(ss, a.C, by == 1.f ? a.eps : 0.f);
-      gn = gh * s / (float)a.C;                // mean(g n)
-      if (ss < __builtin_inff() || by != 1.f) break;
-      by = kSmall;
+    };
+    sums(std::false_type{});
+    float s = factor(ss, a.C, a.eps);
+    if (!(ss < __builtin_inff())) {            // the same for the whole workgroup
       __syncthreads();
+      root = kSmallRoot;
+      sums(std::true_type{});
+      s = factor(ss, a.C, 0.f) * root;
     }
+    const float gn = gh * s / (float)a.C;      // mean(g n)
     const void* ds_ = more && LATE ? row_at<XT>(a.dsum, t) : nullptr;
     void* dx = row_at(a.dx, t, sizeof(XT));
 #pragma unroll
@@ -487,9 +497,9 @@ __global__ __launch_bounds__(NT) void norm_grad_kernel(NormGradArgs a) {
       if (!HELD) load_weights<V>(a.w, a.wt, c, C, w[0]);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const float n = h[j] * by * s;
+        const float n = h[j] * root * s;
         dw[i][j] = fmaf(dy[j], n, dw[i][j]);
-        h[j] = (dy[j] * w[HELD ? i : 0][j] - n * gn) * s * by;
+        h[j] = (dy[j] * w[HELD ? i : 0][j] - n * gn) * root * s;
         if (more) h[j] += ds[j];
       }
       store_as<XT, STREAM>(dx, c, C, h);

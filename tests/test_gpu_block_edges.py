@@ -6,6 +6,8 @@ import numpy as np
 import pytest
 import torch
 
+from tests import block_ref as B
+from tests import serve_ref as R
 from tests.gpu_util import DEV, down, say
 
 pytestmark = pytest.mark.gpu
@@ -30,6 +32,29 @@ def cancelling(T, cout, cin):
     W[:, 0::32], W[:, 17::32] = 128.0, -128.0
     x[:, 0::32] = x[:, 17::32] = 128.0
     return W, x, 14 * cin // 32
+
+
+# ---- the norm and its gradient ----------------------------------------------------------
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("C", [33, 640, 4097, 20000])
+def test_small_elements_beside_large_ones(C, dtype):
+    """Rows whose squares pass fp32's range, with elements 2^-140 of the largest and weights that bring them back."""
+    say("small beside large", C, dtype)
+    g = torch.Generator().manual_seed(5)
+    x = 1e-12 * torch.randn(4, C, generator=g)
+    x[0, 7], x[1, 9], x[2, 0], x[3, C - 1] = 1e30, -3e37, 2e20, 1.0
+    x, w = x.to(dtype), torch.full((C,), 1e20)
+    y, _, _ = lcp.RMSNorm(w.to(DEV), 1e-6, dtype=F32)(x.to(DEV))
+    ref, _, tol = B.rms_norm(x.double().numpy(), None, w.double().numpy(), 1e-6)
+    # an element whose normalised value n is subnormal is off by half of fp32's least number, times the weight
+    low = 2.0 ** -150 * w.double().numpy()
+    assert np.all(np.abs(down(y) - ref) <= tol + R.U32 * np.abs(ref) + low)
+    dy = 1e-25 * torch.randn(4, C, generator=g)
+    dy[:, 5] = 1e15
+    dx, dw = lcp.RMSNorm(torch.ones(C, device=DEV), 1e-6).backward(x.float().to(DEV), dy.to(DEV))
+    rx, rw, tx, tw = B.rms_norm_bwd(x.double().numpy(), dy.double().numpy(), None, np.ones(C), 1e-6)
+    assert np.all(np.abs(down(dx) - rx) <= tx + R.U32 * np.abs(rx) + 2.0 ** -148)
+    assert np.all(np.abs(down(dw) - rw) <= tw + R.U32 * np.abs(rw) + 2.0 ** -149 * np.abs(dy.double().numpy()).sum(0))
 
 
 # ---- the product ----------------------------------------------------------------------
