@@ -213,6 +213,10 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
   const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
   return step(b[0], b[1]);
 }
+// A number that all lanes hold, in a scalar register.
+__device__ __forceinline__ float uniform(float v) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readfirstlane((int)__float_as_uint(v)));
+}
 // The waves' parts in LDS, added in order.
 template <int W>
 __device__ __forceinline__ float sum_of(const float* p) {
@@ -224,10 +228,20 @@ __device__ __forceinline__ float sum_of(const float* p) {
 
 // The factor s from a row's sum of squares. Where that passed fp32's range, h is
 // scaled by kSmall first: the sum then has a square of 1e17 2^-96 or more, of 2^64 at
-// most, and eps is nothing beside it. Half of the scaling (its root) then meets h and half the
-// factor, so that nothing becomes subnormal on the way which is not in the end.
-constexpr float kSmall = 0x1p-96f, kSmallRoot = 0x1p-48f;
+// most, and eps is nothing beside it. Where eps is subnormal and the sum small enough for
+// the squares' lost bits to count beside it, h is scaled by 2^64: eps is then 2^-21 or more.
+// Half of the scaling (its root) then meets h and half the factor, so that nothing becomes
+// subnormal on the way which is not in the end.
 __device__ __forceinline__ float factor(float ss, int C, float eps) { return 1.f / sqrtf(ss / (float)C + eps); }
+// The root of the scaling for a row whose plain sum of squares is ss: 1 for none.
+__device__ __forceinline__ float scaling_root(float ss, float eps) {
+  if (!(ss < __builtin_inff())) return 0x1p-48f;
+  return eps < 0x1p-126f && ss < 0x1p-80f ? 0x1p32f : 1.f;
+}
+// eps for a row scaled by root^2.
+__device__ __forceinline__ float scaled_eps(float eps, float root) {
+  return root > 1.f ? eps * root * root * root * root : 0.f;
+}
 
 // What the registers hold besides a thread's elements (1024 threads leave 128 of them):
 // HELD, the weights, which rows of more than 16384 elements read again; AHEAD, the next
@@ -315,13 +329,14 @@ __global__ __launch_bounds__(NT) void norm_kernel(NormArgs a) {
         if (c < C) store_as<XT, STREAM>(sum, c, C, h[i]);
       }
     }
-    if (!(ss < __builtin_inff())) {            // the same for the whole workgroup
+    const float root = scaling_root(ss, a.eps);
+    if (root != 1.f) {                         // the same for the whole workgroup
       __syncthreads();
-      s = factor(squares(kSmall), a.C, 0.f) * kSmallRoot;
+      s = factor(squares(root * root), a.C, scaled_eps(a.eps, root)) * root;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int j = 0; j < V; ++j) h[i][j] *= kSmallRoot;
+        for (int j = 0; j < V; ++j) h[i][j] *= root;
     }
     uint32_t top = 0;
 #pragma unroll
@@ -471,16 +486,16 @@ __global__ __launch_bounds__(NT) void norm_grad_kernel(NormGradArgs a) {
       gh = wave_sum(gh);
       if ((tid & 63) == 0) { part[turn][0][wave] = ss; part[turn][1][wave] = gh; }
       __syncthreads();
-      ss = sum_of<W>(part[turn][0]);
-      gh = sum_of<W>(part[turn][1]);
+      ss = uniform(sum_of<W>(part[turn][0]));
+      gh = uniform(sum_of<W>(part[turn][1]));
     };
     sums(std::false_type{});
     float s = factor(ss, a.C, a.eps);
-    if (!(ss < __builtin_inff())) {            // the same for the whole workgroup
+    root = scaling_root(ss, a.eps);
+    if (root != 1.f) {                         // the same for the whole workgroup
       __syncthreads();
-      root = kSmallRoot;
       sums(std::true_type{});
-      s = factor(ss, a.C, 0.f) * root;
+      s = factor(ss, a.C, scaled_eps(a.eps, root)) * root;
     }
     const float gn = gh * s / (float)a.C;      // mean(g n)
     const void* ds_ = more && LATE ? row_at<XT>(a.dsum, t) : nullptr;

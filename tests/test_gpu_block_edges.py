@@ -57,6 +57,27 @@ def test_small_elements_beside_large_ones(C, dtype):
     assert np.all(np.abs(down(dw) - rw) <= tw + R.U32 * np.abs(rw) + 2.0 ** -149 * np.abs(dy.double().numpy()).sum(0))
 
 
+@pytest.mark.parametrize("eps", [2.0 ** -126, 1e-40, 3e-43, 1.5e-45])
+def test_subnormal_eps(eps):
+    """Any eps above 0, beside rows whose mean square is as small, or whose squares are no fp32 numbers at all."""
+    say("subnormal eps", eps)
+    C, e = 640, float(np.float32(eps))
+    g = torch.Generator().manual_seed(6)
+    x, dy = torch.randn(9, C, generator=g), torch.randn(9, C, generator=g)
+    x *= torch.tensor([1.0, 1e25, 1e-12, 1e-19, 1e-20, 3e-21, 1e-22, 1e-30, 1e-41])[:, None]
+    x[3, 5] = 0
+    w = torch.rand(C, generator=g) + 0.5
+    norm = lcp.RMSNorm(w.to(DEV), eps)
+    y = down(norm(x.to(DEV))[0])
+    ref, _, tol = B.rms_norm(x.double().numpy(), None, w.double().numpy(), e)
+    assert np.all(np.abs(y - ref) <= tol + R.U32 * np.abs(ref))
+    dy[6:] *= 1e-5                                       # the factor is 1e22 there
+    dx, dw = norm.backward(x.to(DEV), dy.to(DEV))
+    rx, rw, tx, tw = B.rms_norm_bwd(x.double().numpy(), dy.double().numpy(), None, w.double().numpy(), e)
+    assert np.all(np.abs(down(dx) - rx) <= tx + R.U32 * np.abs(rx))
+    assert np.all(np.abs(down(dw) - rw) <= tw + R.U32 * np.abs(rw))
+
+
 # ---- the product ----------------------------------------------------------------------
 @pytest.mark.parametrize("yt", [BF, F32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("dtype", [BF, F8], ids=["bf16", "e4m3"])
