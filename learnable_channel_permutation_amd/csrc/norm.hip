@@ -8,8 +8,6 @@
 // NT threads with NV chunks of 16 bytes each, in registers from the loads to the
 // stores, so that every input is read once; the next row's loads fly during this
 // one's sums. The weight (and the gather's places) are loaded once a workgroup.
-#include <type_traits>
-
 #include "block.h"
 
 namespace lcp {
@@ -463,8 +461,10 @@ __global__ __launch_bounds__(NT) void norm_grad_kernel(NormGradArgs a) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) { ch[i] = nh[i]; cy[i] = ny[i]; cs[i] = ns[i]; }
     if (AHEAD && t + gridDim.x < a.T) load(t + gridDim.x);
-    float root = 1.f, ss, gh;
-    auto sums = [&](auto scaled) {             // of squares, and of g (h root)
+    // Once; once more with h scaled; and once more with g cut where its products' sum with h passes fp32's range, which
+    // their mean over n does not: (g cut) (h root) is at most 2^32 2^80 then.
+    float root = 1.f, cut = 1.f, ss, gh;
+    for (bool first = true;; first = false) {
       ss = gh = 0.f;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
@@ -477,9 +477,9 @@ __global__ __launch_bounds__(NT) void norm_grad_kernel(NormGradArgs a) {
         }
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          const float v = scaled ? h[j] * root : h[j], u = scaled ? v * root : v;
+          const float v = h[j] * root, u = v * root;
           ss = fmaf(u, u, ss);
-          gh = fmaf(dy[j] * w[HELD ? i : 0][j], v, gh);
+          gh = fmaf(dy[j] * cut * w[HELD ? i : 0][j], v, gh);
         }
       }
       ss = wave_sum(ss);
@@ -488,16 +488,14 @@ __global__ __launch_bounds__(NT) void norm_grad_kernel(NormGradArgs a) {
       __syncthreads();
       ss = uniform(sum_of<W>(part[turn][0]));
       gh = uniform(sum_of<W>(part[turn][1]));
-    };
-    sums(std::false_type{});
-    float s = factor(ss, a.C, a.eps);
-    root = scaling_root(ss, a.eps);
-    if (root != 1.f) {                         // the same for the whole workgroup
+      const float need = first ? scaling_root(ss, a.eps) : 1.f;            // the same for the whole workgroup
+      if (need != 1.f) root = need;
+      else if (!(fabsf(gh) < __builtin_inff()) && cut == 1.f) cut = 0x1p-96f;
+      else break;
       __syncthreads();
-      sums(std::true_type{});
-      s = factor(ss, a.C, scaled_eps(a.eps, root)) * root;
     }
-    const float gn = gh * s / (float)a.C;      // mean(g n)
+    const float s = root == 1.f ? factor(ss, a.C, a.eps) : factor(ss, a.C, scaled_eps(a.eps, root)) * root;
+    const float gn = gh * s / (float)a.C / cut;            // mean(g n)
     const void* ds_ = more && LATE ? row_at<XT>(a.dsum, t) : nullptr;
     void* dx = row_at(a.dx, t, sizeof(XT));
 #pragma unroll

@@ -78,6 +78,30 @@ def test_subnormal_eps(eps):
     assert np.all(np.abs(down(dw) - rw) <= tw + R.U32 * np.abs(rw))
 
 
+@pytest.mark.parametrize("dt", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("C", [256, 4097, 20000])
+def test_gradient_of_large_elements_and_large_gradients(C, dt):
+    """Sums of dy h past fp32's range whose means with the normalised h are ordinary numbers."""
+    say("large gradient", C, dt)
+    g = torch.Generator().manual_seed(8)
+    h, dy = torch.randn(6, C, generator=g), torch.randn(6, C, generator=g)
+    h *= torch.tensor([3e16, 1e28, 1e-15, 1e17, 1.0, 1e30])[:, None]
+    dy *= torch.tensor([3e25, 1e35, 1e15, 1e30, 1e36, 1.0])[:, None]
+    h[3] = h[3].abs()
+    dy[3] = dy[3].abs()                                  # the sum does not cancel
+    h, dy, w = h.to(dt), dy.to(dt), torch.rand(C, generator=g) + 0.5
+    dx, dw = lcp.RMSNorm(w.to(DEV), 1e-6).backward(h.to(DEV), dy.to(DEV))
+    rx, rw, tx, tw = B.rms_norm_bwd(h.double().numpy(), dy.double().numpy(), None, w.double().numpy(), 1e-6)
+    half = torch.finfo(dt).eps / 2
+    assert np.isfinite(rx).all() and np.isfinite(rw).all()
+    assert np.all(np.abs(down(dx) - rx) <= tx + half * (np.abs(rx) + tx))
+    assert np.all(np.abs(down(dw) - rw) <= tw + R.U32 * np.abs(rw))
+    dy[1, 3] = float("inf")                              # and what is not finite stays so, in its row alone
+    dx2, _ = lcp.RMSNorm(w.to(DEV), 1e-6).backward(h.to(DEV), dy.to(DEV))
+    assert not bool(torch.isfinite(dx2[1]).any())
+    assert torch.equal(dx2[[0, 2, 3, 4, 5]], dx[[0, 2, 3, 4, 5]])
+
+
 # ---- the product ----------------------------------------------------------------------
 @pytest.mark.parametrize("yt", [BF, F32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("dtype", [BF, F8], ids=["bf16", "e4m3"])
