@@ -198,6 +198,7 @@ class RMSNorm:
 
     weight [C] float32 or bfloat16. perm [C / B, B] int32 (lcp_harden's): the output is in that layer's channel
     order. dtype: the output's, float32, bfloat16 or float8_e4m3fn (with a scale for each token), None for x's.
+    Calls are no part of autograd's graph (they warn where an input asks for a gradient): backward() computes it.
     """
 
     def __init__(self, weight, eps=1e-6, perm=None, dtype=None):

@@ -9,6 +9,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/GradMode.h>
 #include <c10/core/Stream.h>
 #include <c10/core/impl/VirtualGuardImpl.h>
 #include <torch/csrc/Exceptions.h>
@@ -382,6 +383,17 @@ void check_rows(const at::Tensor& t, int64_t T, int64_t C, const char* what) {
   if (t.dim() != 2 || t.size(0) != T || t.size(1) != C || (C > 1 && t.stride(1) != 1)) throw Bad{what};
 }
 
+// These calls are no part of autograd's graph: what they make of tensors that ask for a gradient has none, which
+// the caller (of the Python function above this one) is told.
+void warn_of_no_graph(std::initializer_list<const at::Tensor*> inputs, const char* what) {
+  if (!c10::GradMode::is_enabled()) return;
+  for (const at::Tensor* t : inputs)
+    if (t && t->requires_grad()) {
+      if (PyErr_WarnEx(PyExc_UserWarning, what, 2) < 0) throw Bad{nullptr};
+      return;
+    }
+}
+
 // rms_norm(x, weight, residual, perm, y, scale, sum, y_type, eps, make, stream) ->
 // (status, y, scale, sum). y_type: an lcp_dtype, or -1 for x's; with make, what is
 // None among y, scale (e4m3) and sum (with a residual) is made here.
@@ -428,6 +440,9 @@ PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     f.eps = (float)PyFloat_AsDouble(a[8]);
     if (f.eps == -1.f && PyErr_Occurred()) return nullptr;
     const int gpu = on_gpu({&x, &w, res, perm, y, scale, sum});
+    warn_of_no_graph({&x, &w, res},
+                     "lcp_rms_norm is not part of autograd's graph: its outputs have no gradient (RMSNorm.backward and "
+                     "lcp_rms_norm_bwd compute it); detach its inputs or call it under torch.no_grad()");
     at::Tensor o, sc, su;
     if (y) o = *y;
     else o = at::empty({T, C}, x.options().dtype(e4m3 ? at::kFloat8_e4m3fn : f.y_dt == LCP_F32 ? at::kFloat : at::kBFloat16));
@@ -578,6 +593,9 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
     at::Tensor o, b;
     if (code == LCP_OK) {
       const int gpu = on_gpu({&x, xs, bias, gate, res, y, ws}, p.gpu);
+      warn_of_no_graph({&x, xs, bias, gate, res},
+                       "lcp_sparse_linear has no gradient and is not part of autograd's graph; detach its inputs or call "
+                       "it under torch.no_grad()");
       if (y) o = *y;
       else o = at::empty({T, cout}, x.options().dtype(yt == LCP_F32 ? at::kFloat : at::kBFloat16));
       if (ws) b = *ws;

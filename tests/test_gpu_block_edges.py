@@ -1,6 +1,7 @@
 """Values and calls at the edges of what the documents of a decoder block's operators allow (root-mean-square norm, its
 gradient, the 2:4 product with an epilogue), against their 64-bit definitions."""
 import math
+import warnings
 
 import numpy as np
 import pytest
@@ -100,6 +101,31 @@ def test_gradient_of_large_elements_and_large_gradients(C, dt):
     dx2, _ = lcp.RMSNorm(w.to(DEV), 1e-6).backward(h.to(DEV), dy.to(DEV))
     assert not bool(torch.isfinite(dx2[1]).any())
     assert torch.equal(dx2[[0, 2, 3, 4, 5]], dx[[0, 2, 3, 4, 5]])
+
+
+def test_inputs_that_ask_for_a_gradient():
+    """Results have no graph, and the caller is told so where the call stands; not under no_grad, nor of plain inputs."""
+    x, w = torch.randn(3, 64, device=DEV), torch.ones(64, device=DEV)
+    lin, y = straight(torch.randn(32, 64, device=DEV), BF), torch.empty(3, 64, device=DEV)
+    xb, bias = x.to(BF), torch.zeros(32, device=DEV).to(BF)
+
+    def ask(t):
+        return t.detach().clone().requires_grad_()
+
+    calls = [lambda f: lcp.RMSNorm(w)(f(x)), lambda f: lcp.RMSNorm(f(w))(x), lambda f: lcp.RMSNorm(w)(x, residual=f(x)),
+             lambda f: lcp.lcp_rms_norm(f(x), w, y), lambda f: lin(f(xb)), lambda f: lin(xb, bias=f(bias)),
+             lambda f: lin(xb, gate=f(bias.expand(3, 32).contiguous())), lambda f: lin(xb, residual=f(x[:, :32].contiguous()))]
+    for call in calls:
+        with pytest.warns(UserWarning, match="autograd") as seen:
+            call(ask)
+        assert seen[0].filename == __file__
+        with warnings.catch_warnings():
+            warnings.simplefilter("error")
+            call(lambda t: t)
+            with torch.no_grad():
+                call(ask)
+            with pytest.raises(UserWarning):
+                call(ask)
 
 
 # ---- the product ----------------------------------------------------------------------
