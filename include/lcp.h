@@ -655,6 +655,13 @@ typedef struct lcp_epilogue {
  *   is 0, up to 64 tokens); one workspace serves one call in flight, and one for a
  *   number of tokens serves smaller ones. */
 int lcp_sparse_linear_workspace_bytes(const lcp_packed* w, int T, size_t* bytes);
+
+/* lcp_sparse_linear_cut - how lcp_sparse_linear cuts a call (host only), five numbers:
+ * cut[0]: 0 bf16 instructions on bf16, 1 the same on e4m3, converted, 2 e4m3
+ * instructions; cut[1], cut[2], cut[3]: tiles of 16 rows, tiles of 16 tokens and waves of
+ * a workgroup over all of K, or 0, 0, 0: tiles of 256 rows x 128 tokens, with K in cut[4]
+ * parts, whose sums the workspace holds. */
+int lcp_sparse_linear_cut(const lcp_packed* w, int T, lcp_dtype y_dt, int32_t* cut);
 int lcp_sparse_linear(const lcp_packed* w, const void* x, int64_t x_row,
                       const float* x_scale, int T, const lcp_epilogue* e,
                       void* y, int64_t y_row, lcp_dtype y_dt, void* ws,

@@ -19,7 +19,8 @@ from ._lib import (LCP_BF16, LCP_F32, LcpError, lcp_colnorm, lcp_error,  # noqa:
                    lcp_rope_table, make_kv_cache, make_rope_cfg, lcp_deploy_forward, lcp_gather_channels,
                    lcp_layer_outputs_noalloc, lcp_sparse_gemm, lcp_sparse_pack, lcp_sparse_pack_bytes,
                    lcp_rms_norm, lcp_rms_norm_bwd, lcp_rms_norm_bwd_workspace_bytes, lcp_sparse_linear,
-                   lcp_sparse_linear_workspace_bytes, lcp_sparse_pack_e4m3, lcp_sparse_pack_e4m3_bytes, make_packed)
+                   lcp_sparse_linear_cut, lcp_sparse_linear_workspace_bytes, lcp_sparse_pack_e4m3,
+                   lcp_sparse_pack_e4m3_bytes, make_packed)
 
 __all__ = ["LayerSession", "LcpError", "PagedKVCache", "RMSNorm", "SparseLinear"] + [n for n in _lib.EXPORTS if n in globals()]
 

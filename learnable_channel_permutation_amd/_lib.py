@@ -54,7 +54,7 @@ EXPORTS = [
     "lcp_sparse_gemm", "lcp_deploy_forward", "lcp_rope_table", "lcp_rope", "lcp_kv_append", "lcp_kv_read",
     "lcp_attn_decode_workspace_bytes", "lcp_attn_decode", "lcp_rms_norm", "lcp_rms_norm_bwd_workspace_bytes",
     "lcp_rms_norm_bwd", "lcp_sparse_pack_e4m3_bytes", "lcp_sparse_pack_e4m3", "lcp_sparse_linear_workspace_bytes",
-    "lcp_sparse_linear",
+    "lcp_sparse_linear", "lcp_sparse_linear_cut",
 ]
 
 
@@ -172,6 +172,7 @@ def _load():
         "lcp_sparse_pack_e4m3_bytes": (i, [i, i, psz, psz]),
         "lcp_sparse_pack_e4m3": (i, [vp, i, i, i, vp, vp, vp, vp, vp, vp]),
         "lcp_sparse_linear_workspace_bytes": (i, [ctypes.POINTER(lcp_packed), i, psz]),
+        "lcp_sparse_linear_cut": (i, [ctypes.POINTER(lcp_packed), i, i, vp]),
         "lcp_sparse_linear": (i, [ctypes.POINTER(lcp_packed), vp, ctypes.c_int64, vp, i, ctypes.POINTER(lcp_epilogue), vp,
                                   ctypes.c_int64, i, vp, sz, vp]),
         "lcp_step_workspace_bytes": (i, [i, i, i, i, i, i, psz]),
@@ -528,6 +529,13 @@ def lcp_sparse_linear_workspace_bytes(packed, T):
     _check("lcp_sparse_linear_workspace_bytes",
            LIB.lcp_sparse_linear_workspace_bytes(ctypes.byref(packed), T, ctypes.byref(out)))
     return out.value
+
+
+def lcp_sparse_linear_cut(packed, T, dtype=LCP_BF16):
+    """How a call is cut: (operands, row tiles, token tiles, waves, parts of K), as include/lcp.h lists them."""
+    out = (ctypes.c_int32 * 5)()
+    _check("lcp_sparse_linear_cut", LIB.lcp_sparse_linear_cut(ctypes.byref(packed), T, dtype, out))
+    return tuple(out)
 
 
 def act_code(act):

@@ -77,6 +77,8 @@ struct LinearArgs {
   float* ws;
 };
 size_t sparse_linear_workspace_bytes(const PackedArgs& w, int T);
+// SparseMode, row tiles, token tiles, waves, parts (as lcp_sparse_linear_cut)
+void sparse_linear_cut(const PackedArgs& w, int T, int y_f32, int* out);
 hipError_t launch_sparse_linear(const LinearArgs& a, hipStream_t s);
 
 }  // namespace lcp

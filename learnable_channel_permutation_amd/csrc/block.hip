@@ -174,6 +174,16 @@ int lcp_sparse_linear_workspace_bytes(const lcp_packed* w, int T, size_t* bytes)
   return LCP_OK;
 }
 
+int lcp_sparse_linear_cut(const lcp_packed* w, int T, lcp_dtype y_dt, int32_t* cut) {
+  PackedArgs p;
+  const int rc = check_packed(w, &p);
+  if (rc != LCP_OK) return rc;
+  if (!cut || T <= 0) return LCP_E_INVAL;
+  if (!float_type(y_dt)) return LCP_E_UNSUPPORTED;
+  sparse_linear_cut(p, T, y_dt == LCP_F32, cut);
+  return LCP_OK;
+}
+
 int lcp_sparse_linear(const lcp_packed* w, const void* x, int64_t x_row, const float* x_scale, int T,
                       const lcp_epilogue* e, void* y, int64_t y_row, lcp_dtype y_dt, void* ws, size_t ws_bytes,
                       void* stream) {

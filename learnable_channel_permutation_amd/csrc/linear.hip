@@ -482,7 +482,7 @@ hipError_t launch_sparse_pack_e4m3(const uint16_t* W, int cout, int cin, int B, 
 namespace {
 
 // How a product is cut: RT x NT tiles of 16 rows x 16 tokens and W waves a workgroup, or
-// (RT 0) 256 x 128 tiles with K in `parts`.
+// (RT 0) 256 x 128 tiles with K in `parts`, each of which has steps.
 struct Cut {
   int rt, nt, w, parts;
 };
@@ -547,8 +547,10 @@ Cut cut_for(const LinearArgs& a, int mode) {
   }
   if (a.T < kTilesFrom) return best;
   const int64_t steps = ((int64_t)a.w.cin * (mode == M_BF16 ? 2 : 1) + 127) / 128;
-  for (int parts = 1; parts <= kMostParts; ++parts) {
-    if (parts > steps || (parts > 1 && (int64_t)parts * a.T * a.w.cout * 4 > kMostPartBytes)) break;
+  for (int most = 1; most <= kMostParts; ++most) {
+    const int64_t each = (steps + most - 1) / most;
+    const int parts = (int)((steps + each - 1) / each);
+    if (most > steps || (parts > 1 && (int64_t)parts * a.T * a.w.cout * 4 > kMostPartBytes)) break;
     const double us = tiles_us(a, mode, steps, parts);
     if (us < least) { least = us; best = {0, 0, 0, parts}; }
   }
@@ -577,7 +579,6 @@ hipError_t run_tiles(const LinearArgs& a, int parts, hipStream_t s) {
     return hipGetLastError();
   }
   const int steps = (all + parts - 1) / parts;
-  parts = (all + steps - 1) / steps;           // each has steps
   spgemm_kernel<MODE, SP_RS, NPRE, SP_LSPAN><<<grid(G * parts), SP_NT, SP_LDS<MODE>, s>>>(
       a.w.vals, a.w.meta, a.x.p, a.x.row, a.T, a.w.cout, a.w.cin, steps, Part{a.ws, a.T, a.w.cout, 0});
   const hipError_t e = hipGetLastError();
@@ -610,6 +611,14 @@ hipError_t run_linear(const LinearArgs& a, hipStream_t s) {
   return hipErrorInvalidConfiguration;
 }
 
+// e4m3: exact products, but where the layer's user asked for the e4m3 instructions, whose dropped bits are the whole
+// result where sums cancel; not for fp32 outputs, nor for few tokens, where exact products cost nothing (us,
+// converted against e4m3 instructions: 64 tokens of 4096 <- 4096 5.8 / 5.5, 128 8.6 / 7.6; 4096 tokens of
+// 28672 <- 8192 747 / 541).
+int mode_for(const PackedArgs& w, int T, int y_f32) {
+  if (!w.fp8) return M_BF16;
+  return !w.fast || y_f32 || T < kTilesFrom ? M_E4M3 : M_E4M3_FAST;
+}
 }  // namespace
 
 size_t sparse_linear_workspace_bytes(const PackedArgs& w, int T) {
@@ -618,14 +627,22 @@ size_t sparse_linear_workspace_bytes(const PackedArgs& w, int T) {
   return (size_t)((most + 255) / 256 * 256);
 }
 
-// e4m3: exact products, but where the layer's user asked for the e4m3 instructions, whose dropped bits are the whole
-// result where sums cancel; not for fp32 outputs, nor for few tokens, where exact products cost nothing (us,
-// converted against e4m3 instructions: 64 tokens of 4096 <- 4096 5.8 / 5.5, 128 8.6 / 7.6; 4096 tokens of
-// 28672 <- 8192 747 / 541).
+void sparse_linear_cut(const PackedArgs& w, int T, int y_f32, int* out) {
+  LinearArgs a{};
+  a.w = w;
+  a.T = T;
+  out[0] = mode_for(w, T, y_f32);
+  const Cut c = cut_for(a, out[0]);
+  out[1] = c.rt;
+  out[2] = c.nt;
+  out[3] = c.w;
+  out[4] = c.parts;
+}
+
 hipError_t launch_sparse_linear(const LinearArgs& a, hipStream_t s) {
-  if (!a.w.fp8) return run_linear<M_BF16>(a, s);
-  if (!a.w.fast || a.e.y_f32 || a.T < kTilesFrom) return run_linear<M_E4M3>(a, s);
-  return run_linear<M_E4M3_FAST>(a, s);
+  const int mode = mode_for(a.w, a.T, a.e.y_f32);
+  if (mode == M_BF16) return run_linear<M_BF16>(a, s);
+  return mode == M_E4M3 ? run_linear<M_E4M3>(a, s) : run_linear<M_E4M3_FAST>(a, s);
 }
 
 }  // namespace lcp
