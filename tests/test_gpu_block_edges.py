@@ -103,6 +103,76 @@ def test_gradient_of_large_elements_and_large_gradients(C, dt):
     assert torch.equal(dx2[[0, 2, 3, 4, 5]], dx[[0, 2, 3, 4, 5]])
 
 
+def guarded(n, dtype):
+    """(the whole buffer, n elements inside it): what lies around them is 7 in every byte."""
+    size = torch.empty(0, dtype=dtype).element_size()
+    buf = torch.full((n * size + 512,), 7, dtype=torch.uint8, device=DEV)
+    return buf, buf[256:256 + n * size].view(dtype)
+
+
+def untouched(buf):
+    return bool((buf[:256] == 7).all() and (buf[-256:] == 7).all())
+
+
+@pytest.mark.parametrize("dt,wt", [(BF, BF), (BF, F32), (F32, F32), (F32, BF)], ids=["bf16", "bf16-f32", "f32", "f32-bf16"])
+@pytest.mark.parametrize("T,C", [(1, 1), (1, 3), (2, 33), (65, 1025), (300, 521), (1100, 322), (9, 4097), (3, 8190), (3, 11007),
+                                 (2, 28670), (2, 32767), (2, 32768)])
+def test_nothing_around_the_gradients_outputs(T, C, dt, wt):
+    """What lies around dx, dweight and the workspace, also where rows end inside the last thread's elements; and the
+    results, to tolerances of the sums as they are made: a thread adds 32 of 32768 elements (1024 threads), then six steps
+    of its wave and at most sixteen waves."""
+    say("gradient guards", T, C, dt, wt)
+    g = torch.Generator().manual_seed(C)
+    h, dy = (torch.randn(T, C, generator=g).to(dt) for _ in range(2))
+    w = (1 + 0.3 * torch.randn(C, generator=g)).to(wt)
+    need = lcp.lcp_rms_norm_bwd_workspace_bytes(T, C)
+    (bx, dx), (bw, dw), (bs, ws) = guarded(T * C, dt), guarded(C, wt), guarded(need, torch.uint8)
+    lcp.lcp_rms_norm_bwd(h.to(DEV), w.to(DEV), dy.to(DEV), dx.view(T, C), dw, ws, eps=1e-5)
+    assert untouched(bx) and untouched(bw) and untouched(bs)
+    h, dy, w = (t.double().numpy() for t in (h, dy, w))
+    s = 1 / np.sqrt((h * h).mean(-1, keepdims=True) + 1e-5)
+    n, gw = h * s, dy * w
+    rx, rw = s * (gw - n * (gw * n).mean(-1, keepdims=True)), (dy * n).sum(0)
+    adds, part = 32 + 6 + 16, np.abs(gw * n).mean(-1, keepdims=True)
+    # s: half of its sum's roundings, a mean, a root, a division; the mean of g n: its sum's and five products'; three more
+    tx = R.U32 * s * ((adds / 2 + 8) * np.abs(gw) + (1.5 * adds + 20) * np.abs(n) * part)
+    # terms by s and three products; a workgroup's rows one after the other, then 32 shares of the workgroups and their join
+    rows = -(-T // min(T, 256)) + 1024 // 32 + 32
+    tw = (adds / 2 + 10 + rows) * R.U32 * np.abs(dy * n).sum(0)
+    for got, want, tol, t in ((down(dx).reshape(T, C), rx, tx, dt), (down(dw), rw, tw, wt)):
+        half = torch.finfo(t).eps / 2
+        assert np.all(np.abs(got - want) <= tol + half * (np.abs(want) + tol) + 2.0 ** -140)
+
+
+@pytest.mark.parametrize("xt", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("T,C,Bs", [(1, 1, 0), (3, 33, 0), (70, 1025, 0), (5, 4096, 64), (5, 4097, 0), (3, 13824, 128), (2, 32767, 0),
+                                    (2, 32768, 64), (5000, 96, 32)])
+def test_nothing_around_the_norms_outputs(T, C, Bs, xt):
+    """What lies around the codes, their scales and the sum; and fp32 outputs to a tolerance of the sums as they are made."""
+    say("norm guards", T, C, Bs, xt)
+    g = torch.Generator().manual_seed(C)
+    x, r = (torch.randn(T, C, generator=g).to(xt) for _ in range(2))
+    w = 1 + 0.3 * torch.randn(C, generator=g)
+    perm = torch.stack([torch.randperm(Bs, generator=g) for _ in range(C // Bs)]).int() if Bs else None
+    p = None if perm is None else perm.to(DEV)
+    (by, y), (bc, scale), (bs, total) = guarded(T * C, torch.uint8), guarded(T, F32), guarded(T * C, xt)
+    lcp.lcp_rms_norm(x.to(DEV), w.to(DEV), y.view(F8).view(T, C), scale=scale, residual=r.to(DEV), sum_out=total.view(T, C),
+                     perm=p, eps=1e-5)
+    assert untouched(by) and untouched(bc) and untouched(bs)
+    b32, y32 = guarded(T * C, F32)
+    lcp.lcp_rms_norm(x.to(DEV), w.to(DEV), y32.view(T, C), residual=r.to(DEV), perm=p, eps=1e-5)
+    assert untouched(b32)
+    ref, h, _ = B.rms_norm(x.double().numpy(), r.double().numpy(), w.double().numpy(), 1e-5, None if perm is None else perm.numpy())
+    y32 = down(y32).reshape(T, C)
+    # half of the sum's roundings (54 additions, as above, of squares of h rounded once), the factor's four, h's and two products'
+    tol = ((32 + 6 + 16) / 2 + 9) * R.U32 * np.abs(ref) + 2.0 ** -140
+    assert np.all(np.abs(y32 - ref) <= tol)
+    half = torch.finfo(xt).eps / 2
+    assert np.all(np.abs(down(total).reshape(T, C) - h) <= (R.U32 + half) * (1 + R.U32) * np.abs(h))
+    codes, s = R.quantise(y32.astype(np.float32), "fp8")               # of the very numbers that the kernel rounds
+    assert np.array_equal(y.view(T, C).cpu().numpy(), codes) and np.array_equal(scale.cpu().numpy(), s)
+
+
 def test_inputs_that_ask_for_a_gradient():
     """Results have no graph, and the caller is told so where the call stands; not under no_grad, nor of plain inputs."""
     x, w = torch.randn(3, 64, device=DEV), torch.ones(64, device=DEV)
