@@ -81,10 +81,15 @@ class MlpBlock:
 
 
 def codes(a):
-    """bf16 rows as e4m3 codes with a power of two as scale, in plain torch."""
-    top = a.float().abs().amax(-1).clamp(min=1e-30)
-    scale = torch.exp2(torch.ceil(torch.log2(top / 448.0)))
-    return (a.float() / scale[:, None]).to(torch.float8_e4m3fn), scale
+    """Rows as e4m3 codes and scales by the rule of the operators (include/lcp.h, E4M3 rows), in plain torch: a product's
+    epilogue does not see the maximum of a whole row."""
+    a = a.float()
+    top = a.abs().amax(-1)
+    finite = torch.isfinite(top)
+    m, e = torch.frexp(torch.where(finite, top, 1.0))
+    power = torch.where(top > 0, e - 9 + (m > 0.875), -126).clamp(min=-126)
+    scale = torch.where(finite, torch.ldexp(torch.ones_like(top), power), torch.nan)
+    return torch.where(finite[:, None], a / scale[:, None], 0.0).to(torch.float8_e4m3fn), scale
 
 
 def reference(blk, x, r):
