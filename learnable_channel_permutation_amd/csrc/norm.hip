@@ -211,10 +211,6 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
   const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
   return step(b[0], b[1]);
 }
-// A number that all lanes hold, in a scalar register.
-__device__ __forceinline__ float uniform(float v) {
-  return __uint_as_float((uint32_t)__builtin_amdgcn_readfirstlane((int)__float_as_uint(v)));
-}
 // The waves' parts in LDS, added in order.
 template <int W>
 __device__ __forceinline__ float sum_of(const float* p) {
@@ -224,21 +220,21 @@ __device__ __forceinline__ float sum_of(const float* p) {
   return v;
 }
 
-// The factor s from a row's sum of squares. Where that passed fp32's range, h is
-// scaled by kSmall first: the sum then has a square of 1e17 2^-96 or more, of 2^64 at
-// most, and eps is nothing beside it. Where eps is subnormal and the sum small enough for
-// the squares' lost bits to count beside it, h is scaled by 2^64: eps is then 2^-21 or more.
-// Half of the scaling (its root) then meets h and half the factor, so that nothing becomes
-// subnormal on the way which is not in the end.
+// The factor s from a row's sum of squares. Where that passed fp32's range, h is scaled by
+// 2^-96 for it: the sum then has a square of 1e17 2^-96 or more, of 2^64 at most, and
+// eps is nothing beside it. Where eps is subnormal and the sum small enough for the squares'
+// lost bits to count beside it, h is scaled by 2^64: eps is then 2^-21 or more. The factor
+// that meets the row is the unscaled one: it is subnormal, and keeps 21 bits of 24, only
+// where the mean square passes 2^252.
 __device__ __forceinline__ float factor(float ss, int C, float eps) { return 1.f / sqrtf(ss / (float)C + eps); }
 // The root of the scaling for a row whose plain sum of squares is ss: 1 for none.
 __device__ __forceinline__ float scaling_root(float ss, float eps) {
   if (!(ss < __builtin_inff())) return 0x1p-48f;
   return eps < 0x1p-126f && ss < 0x1p-80f ? 0x1p32f : 1.f;
 }
-// eps for a row scaled by root^2.
-__device__ __forceinline__ float scaled_eps(float eps, float root) {
-  return root > 1.f ? eps * root * root * root * root : 0.f;
+// The factor of a row scaled by root^2 (its sum of squares ss), over root.
+__device__ __forceinline__ float scaled_factor(float ss, int C, float eps, float root) {
+  return factor(ss, C, root > 1.f ? eps * root * root * root * root : 0.f) * root;
 }
 
 // What the registers hold besides a thread's elements (1024 threads leave 128 of them):
@@ -330,11 +326,7 @@ __global__ __launch_bounds__(NT) void norm_kernel(NormArgs a) {
     const float root = scaling_root(ss, a.eps);
     if (root != 1.f) {                         // the same for the whole workgroup
       __syncthreads();
-      s = factor(squares(root * root), a.C, scaled_eps(a.eps, root)) * root;
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < V; ++j) h[i][j] *= root;
+      s = scaled_factor(squares(root * root), a.C, a.eps, root) * root;
     }
     uint32_t top = 0;
 #pragma unroll
@@ -461,41 +453,70 @@ __global__ __launch_bounds__(NT) void norm_grad_kernel(NormGradArgs a) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) { ch[i] = nh[i]; cy[i] = ny[i]; cs[i] = ns[i]; }
     if (AHEAD && t + gridDim.x < a.T) load(t + gridDim.x);
-    // Once; once more with h scaled; and once more with g cut where its products' sum with h passes fp32's range, which
-    // their mean over n does not: (g cut) (h root) is at most 2^32 2^80 then.
-    float root = 1.f, cut = 1.f, ss, gh;
-    for (bool first = true;; first = false) {
-      ss = gh = 0.f;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        float h[V], dy[V];
-        unpack<XT>(ch[i], h);
-        unpack<XT>(cy[i], dy);
-        if (!HELD) {
-          __builtin_amdgcn_sched_barrier(0);
-          load_weights<V>(a.w, a.wt, (i * NT + tid) * V, C, w[0]);
-        }
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const float v = h[j] * root, u = v * root;
-          ss = fmaf(u, u, ss);
-          gh = fmaf(dy[j] * cut * w[HELD ? i : 0][j], v, gh);
-        }
-      }
+    // the waves' shares of both sums, joined
+    auto joined = [&](float& ss, float& gh) {
       ss = wave_sum(ss);
       gh = wave_sum(gh);
       if ((tid & 63) == 0) { part[turn][0][wave] = ss; part[turn][1][wave] = gh; }
       __syncthreads();
-      ss = uniform(sum_of<W>(part[turn][0]));
-      gh = uniform(sum_of<W>(part[turn][1]));
-      const float need = first ? scaling_root(ss, a.eps) : 1.f;            // the same for the whole workgroup
-      if (need != 1.f) root = need;
-      else if (!(fabsf(gh) < __builtin_inff()) && cut == 1.f) cut = 0x1p-96f;
-      else break;
-      __syncthreads();
+      ss = sum_of<W>(part[turn][0]);
+      gh = sum_of<W>(part[turn][1]);
+    };
+    float ss = 0.f, gh = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float h[V], dy[V];
+      unpack<XT>(ch[i], h);
+      unpack<XT>(cy[i], dy);
+      if (!HELD) {
+        __builtin_amdgcn_sched_barrier(0);
+        load_weights<V>(a.w, a.wt, (i * NT + tid) * V, C, w[0]);
+      }
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        ss = fmaf(h[j], h[j], ss);
+        gh = fmaf(dy[j] * w[HELD ? i : 0][j], h[j], gh);
+      }
     }
-    const float s = root == 1.f ? factor(ss, a.C, a.eps) : factor(ss, a.C, scaled_eps(a.eps, root)) * root;
-    const float gn = gh * s / (float)a.C / cut;            // mean(g n)
+    joined(ss, gh);
+    float s = factor(ss, a.C, a.eps), gn = gh * s / (float)a.C;            // gn: mean(g n)
+    const float root = scaling_root(ss, a.eps);
+    if (root != 1.f || !(fabsf(gh) < __builtin_inff())) {                  // the same for the whole workgroup
+      // Once more with h scaled; and once more with g cut where their products' sum passes fp32's range, which their
+      // mean over n does not: (g cut) (h root) is at most 2^32 2^80 then. From memory, a chunk at a time: such rows
+      // are few, and what they hold in registers all rows would.
+      const void *h_ = row_at<XT>(a.h, t), *dy_ = row_at<XT>(a.dy, t);
+      float cut = root != 1.f ? 1.f : 0x1p-96f;
+      for (;;) {
+        __syncthreads();
+        ss = gh = 0.f;
+#pragma nounroll
+        for (uint32_t c = tid * V; c < C; c += NT * V) {
+          float h[V], dy[V], w[V];
+          unpack<XT>(load_chunk<XT, false>(h_, c, C), h);
+          unpack<XT>(load_chunk<XT, false>(dy_, c, C), dy);
+          load_weights<V>(a.w, a.wt, c, C, w);
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            const float v = h[j] * root, u = v * root;
+            ss = fmaf(u, u, ss);
+            gh = fmaf(dy[j] * cut * w[j], v, gh);
+          }
+        }
+        joined(ss, gh);
+        if (fabsf(gh) < __builtin_inff() || cut != 1.f) break;
+        cut = 0x1p-96f;
+      }
+      if (root != 1.f) s = scaled_factor(ss, a.C, a.eps, root);
+      gn = gh * s / (float)a.C / cut;
+      s *= root;
+    }
+    // Elements are unpacked again below: kept as fp32 since the sums they would take the registers of 1024 threads
+    // (with and without, us: 2000 x 28672 bf16 135 / 191, 700 x 11008 fp32 34 / 44; of 64 threads 16384 x 512 23.8 / 22.9).
+    if constexpr (NT == 1024) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) asm volatile("" : "+v"(ch[i]), "+v"(cy[i]));
+    }
     const void* ds_ = more && LATE ? row_at<XT>(a.dsum, t) : nullptr;
     void* dx = row_at(a.dx, t, sizeof(XT));
 #pragma unroll
@@ -510,9 +531,9 @@ __global__ __launch_bounds__(NT) void norm_grad_kernel(NormGradArgs a) {
       if (!HELD) load_weights<V>(a.w, a.wt, c, C, w[0]);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const float n = h[j] * root * s;
+        const float n = h[j] * s;
         dw[i][j] = fmaf(dy[j], n, dw[i][j]);
-        h[j] = (dy[j] * w[HELD ? i : 0][j] - n * gn) * root * s;
+        h[j] = (dy[j] * w[HELD ? i : 0][j] - n * gn) * s;
         if (more) h[j] += ds[j];
       }
       store_as<XT, STREAM>(dx, c, C, h);

@@ -58,6 +58,28 @@ def test_small_elements_beside_large_ones(C, dtype):
     assert np.all(np.abs(down(dw) - rw) <= tw + R.U32 * np.abs(rw) + 2.0 ** -149 * np.abs(dy.double().numpy()).sum(0))
 
 
+@pytest.mark.parametrize("dt", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("C", [33, 4097, 8192, 11008, 28672])
+def test_rows_of_the_largest_numbers(C, dt):
+    """Every element near fp32's largest: the factor is 2^-127 or less and keeps 21 bits, off by 2^-22 at most."""
+    say("largest numbers", C, dt)
+    g = torch.Generator().manual_seed(9)
+    h = 3.3e38 * (1 - 0.2 * torch.rand(3, C, generator=g)) * torch.sign(torch.randn(3, C, generator=g))
+    h[1] *= 0.3
+    h, dy = h.to(dt), torch.randn(3, C, generator=g).to(dt)
+    w = torch.rand(C, generator=g) + 0.5
+    norm = lcp.RMSNorm(w.to(DEV), 1e-6, dtype=F32)
+    ref, _, tol = B.rms_norm(h.double().numpy(), None, w.double().numpy(), 1e-6)
+    y = down(norm(h.to(DEV))[0])
+    assert np.all(np.abs(y - ref) <= tol + (R.U32 + 2.0 ** -22) * np.abs(ref))
+    dx, dw = norm.backward(h.to(DEV), dy.to(DEV))
+    rx, rw, tx, tw = B.rms_norm_bwd(h.double().numpy(), dy.double().numpy(), None, w.double().numpy(), 1e-6)
+    # dx is about 1e-38: its rounding is half a step, eps / 2 of a normal number and half of the least of a subnormal one
+    half, least = torch.finfo(dt).eps / 2, torch.finfo(dt).smallest_normal * torch.finfo(dt).eps
+    assert np.all(np.abs(down(dx) - rx) <= tx + (2.0 ** -20 + half) * np.abs(rx) + least)
+    assert np.all(np.abs(down(dw) - rw) <= tw + R.U32 * np.abs(rw) + 2.0 ** -22 * 3 * np.abs(dy.double().numpy()).sum(0))
+
+
 @pytest.mark.parametrize("eps", [2.0 ** -126, 1e-40, 3e-43, 1.5e-45])
 def test_subnormal_eps(eps):
     """Any eps above 0, beside rows whose mean square is as small, or whose squares are no fp32 numbers at all."""
