@@ -238,7 +238,7 @@ class SparseLinear:
     them. Inputs are in the layer's permuted channel order (RMSNorm with perm, lcp_gather_channels, or a layer whose
     rows were packed in that order). The tensors are the layer's for its life.
     Products are exact and sums float32. fast=True, for 8-bit layers, lets bfloat16 outputs of more than 64 tokens come
-    from the e4m3 matrix instructions, a third faster; a sum far smaller than its terms may then be all error.
+    from the e4m3 matrix instructions, up to a third faster; a sum far smaller than its terms may then be all error.
     """
 
     def __init__(self, vals, meta, cout, cin, scale=None, fast=False):

@@ -514,7 +514,8 @@ constexpr int kTilesFrom = 65;
 // The estimates that choose, in us, fitted to 351 calls (4096 <- 4096, 11008 <- 4096, 4096 <- 11008,
 // 5120 <- 13824, 13824 <- 5120, 28672 <- 8192, 8192 <- 28672, 6400 <- 2720, 2080 <- 9600; 24 to 1000
 // tokens; each mode): the chosen cut is 1.2 % slower than the best measured one in the mean, over
-// 10 % at 16 calls, 23 % at one. A workgroup of the thin kernel takes in 80 KB a us, a tile's
+// 10 % at 16 calls, 23 % at one. No call was held out of the fit, and past 1000 tokens it is
+// carried on. A workgroup of the thin kernel takes in 80 KB a us, a tile's
 // step takes 0.46 us (e4m3 0.53, converted 0.82), and what a call takes follows from the rounds
 // of 256 workgroups. Measured, us: 128 tokens of 4096 <- 4096 bf16 2 x 4 x 8 11.0, 4 x 4 x 8 13.1, tiles
 // in four parts 18.2; 200 4 x 4 x 8 13.4, 2 x 4 x 8 18.7; 100 of 11008 <- 4096 6 x 4 x 4 18.6, 4 x 4 x 4 21.3,
@@ -630,8 +631,8 @@ hipError_t run_linear(const LinearArgs& a, hipStream_t s) {
 
 // e4m3: exact products, but where the layer's user asked for the e4m3 instructions, whose dropped bits are the whole
 // result where sums cancel; not for fp32 outputs, nor for few tokens, where exact products cost nothing (us,
-// converted against e4m3 instructions: 64 tokens of 4096 <- 4096 5.8 / 5.5, 128 8.6 / 7.6; 4096 tokens of
-// 28672 <- 8192 747 / 541).
+// converted against e4m3 instructions: 64 tokens of 4096 <- 4096 5.8 / 5.5, 128 8.6 / 7.6; random operands, 1000
+// tokens of 11008 <- 4096 85 / 67, 4096 of 28672 <- 8192 965 / 640).
 int mode_for(const PackedArgs& w, int T, int y_f32) {
   if (!w.fp8) return M_BF16;
   return !w.fast || y_f32 || T < kTilesFrom ? M_E4M3 : M_E4M3_FAST;

@@ -576,9 +576,10 @@ __global__ __launch_bounds__(256) void norm_dw_kernel(const float* part, int row
 // 256 x 4 134, 512 x 2 98, 1024 x 1 147; 8192 x 8192 256 x 4 94, 512 x 2 89, 1024 x 1 89; 5000
 // x 13824 512 x 4 112, 1024 x 2 93. fp32 2049 x 4097 256 x 8 17.1, 512 x 4 13.0, 1024 x 2 15.7.
 // 512 x 1 and 256 x 2 (768 workgroups): 1 x 4096 3.0 and 3.4; 200 x 4096 3.5 and 4.0; 2000 x 4096
-// 11.5 and 12.4; 10000 x 4096 59.6 and 60.1, x 2560 39.6 and 40.6. Gradient, with 256 workgroups: 8191 x
-// 8192 256 x 4 93, 512 x 2 92; 5000 x 13824 512 x 4 155, 1024 x 2 129; 16384 x 4096 256 x 2 95, 512 x 1
-// 98, fp32 x 2048 93 and 88.
+// 11.5 and 12.4; 10000 x 4096 59.6 and 60.1, x 2560 39.6 and 40.6. Gradient with dsum, 256 workgroups (us):
+// 8191 x 8192 256 x 4 193, 512 x 2 91; 5000 x 13824 512 x 4 148, 1024 x 2 106; 16384 x 4096 256 x 2 99, 512 x 1
+// 88; fp32 16384 x 2048 256 x 2 88, 512 x 1 91, 2049 x 4097 512 x 4 37, 1024 x 2 34, 5000 x 8192 512 x 4
+// 113.6, 1024 x 2 114.0: one rule for both serves them within 10 %.
 struct Shape {
   int nt, nv;
 };
@@ -596,8 +597,8 @@ Shape shape_of(int C) {
 constexpr int64_t kStreamBytes = (int64_t)256 << 20;
 
 // Workgroups of the gradient, each of which leaves a row in the workspace: 256 / 512
-// / 1024, us: 8191 x 8192 92 / 95 / -, 16384 x 4096 100 / 102 / -, 16384 x 2048 68 / 53 / 60, 16384 x
-// 512 59 / 35 / 23.
+// / 1024 / 2048, us, with dsum: 8191 x 8192 91 / 94, 16384 x 4096 89 / 93, 16384 x 2048 70 / 49 / 54, 16384 x
+// 512 - / 35 / 22.9 / 20.3 (the last for a workspace of twice the size).
 int grad_rows(int T, int C) {
   const int most = C <= 512 ? 1024 : C <= 2048 ? 512 : 256;
   return T < most ? T : most;
