@@ -331,3 +331,100 @@ def test_activations_relative_to_their_values(act, yt):
         y = down(lin(x[rows].to(DEV), act=act, dtype=yt))[:, :8]
         r = ref[rows.numpy()]
         assert np.all(np.abs(y - r) <= tol * np.abs(r) + 2.0 ** -118)
+
+
+def operands(T, cout, cin, dtype, seed):
+    """(layer, x, scale) of random numbers, in the weights' own order."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    W, x, s = 0.1 * torch.randn(cout, cin, generator=g, device=DEV), torch.randn(T, cin, generator=g, device=DEV), None
+    lin = straight(W, dtype)
+    if dtype == F8:
+        x, s, _ = lcp.RMSNorm(torch.ones(cin, device=DEV), dtype=F8)(x)
+    else:
+        x = x.to(BF)
+    return lin, x, s
+
+
+@pytest.mark.parametrize("dtype", [BF, F8], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("T", [2, 17, 64, 100, 400, 1300])
+def test_rows_that_share_memory(T, dtype):
+    """One row for all tokens (stride 0) as x, gate and residual gives what T copies of it give."""
+    lin, x, s = operands(1, 544, 352, dtype, 3)
+    g = torch.Generator(device=DEV).manual_seed(4)
+    gate, res = (torch.randn(1, 544, generator=g, device=DEV).to(BF) for _ in range(2))
+    s = None if s is None else s.expand(T).contiguous()
+    for yt in (BF, F32):
+        kw = dict(scale=s, act="silu", dtype=yt)
+        want = lin(x.repeat(T, 1), gate=gate.repeat(T, 1), residual=res.repeat(T, 1), **kw)
+        assert torch.equal(lin(x.expand(T, -1), gate=gate.expand(T, -1), residual=res.expand(T, -1), **kw), want)
+
+
+@pytest.mark.parametrize("dtype", [BF, F8], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("T", [1, 40, 300, 1000])
+def test_position_words_at_any_word(T, dtype):
+    """meta begins at a multiple of 4 bytes, as it may."""
+    lin, x, s = operands(T, 544, 1056, dtype, 5)
+    for yt in (BF, F32):
+        want = lin(x, scale=s, dtype=yt)
+        for off in (1, 2, 3):
+            m = torch.empty(lin.meta.numel() + 4, dtype=torch.int32, device=DEV)[off:off + lin.meta.numel()]
+            m.copy_(lin.meta)
+            assert torch.equal(lcp.SparseLinear(lin.vals, m, 544, 1056, lin.scale)(x, scale=s, dtype=yt), want)
+
+
+@pytest.mark.parametrize("fast", [False, True], ids=["exact", "fast"])
+@pytest.mark.parametrize("yt", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("T", [1, 19, 70, 400])
+def test_nan_codes(T, yt, fast):
+    """A NaN code at a kept position makes its token's outputs NaN where the weight is kept (0 times NaN, too), and no other's;
+    at a pruned one it is not read."""
+    W = torch.randn(64, 288, generator=torch.Generator(device=DEV).manual_seed(6), device=DEV)
+    lin = straight(W, F8, fast=fast)
+    _, x, s = operands(T, 32, 288, F8, 7)
+    clean = lin(x, scale=s, dtype=yt)
+    bad = x.clone()
+    bad.view(torch.uint8)[T // 2, 161] = 0x7f            # position 1 of its group: kept
+    bad.view(torch.uint8)[0, 6] = 0xff                   # position 2: pruned
+    y = lin(bad, scale=s, dtype=yt)
+    assert bool(torch.isnan(y[T // 2]).all())
+    rest = torch.arange(T, device=DEV) != T // 2
+    assert torch.equal(y[rest], clean[rest]) and bool(torch.isfinite(clean).all())
+
+
+def test_one_token_of_any_stride():
+    """The stride of a single row is no address: it may be anything, also where more rows would have to be aligned."""
+    for dtype in (BF, F8):
+        lin, x, s = operands(1, 96, 64, dtype, 8)
+        want = lin(x, scale=s)
+        for stride in (0, 1, 67, 1 << 39):
+            out = torch.zeros(1, 96, dtype=BF, device=DEV)
+            got = lin(x.as_strided((1, 64), (stride, 1)), scale=s, residual=out.as_strided((1, 96), (stride, 1)),
+                      out=out.as_strided((1, 96), (stride, 1)))
+            assert torch.equal(got, want) and torch.equal(out, want)
+    x, w = torch.randn(1, 77, device=DEV), torch.ones(77, device=DEV)
+    want, _, _ = lcp.RMSNorm(w)(x)
+    dx, dw = lcp.RMSNorm(w).backward(x, x)
+    for stride in (0, 1, 1 << 39):
+        v = x.as_strided((1, 77), (stride, 1))
+        y = torch.empty(77, device=DEV).as_strided((1, 77), (stride, 1))
+        assert torch.equal(lcp.RMSNorm(w)(v, out=y)[0], want)
+        a, b = lcp.RMSNorm(w).backward(v, v, dx=y)
+        assert torch.equal(a, dx) and torch.equal(b, dw)
+
+
+@pytest.mark.parametrize("Bs", [32, 64, 128])
+def test_orders_are_read_modulo_their_blocks(Bs):
+    """Entries beyond a block or below 0, in the norm and in both packings."""
+    C = 384
+    g = torch.Generator().manual_seed(Bs)
+    perm = torch.stack([torch.randperm(Bs, generator=g) for _ in range(C // Bs)])
+    other = perm + Bs * torch.randint(-3, 4, perm.shape, generator=g)
+    other[0, 0] = perm[0, 0] - (1 << 31)
+    perm, other = perm.int().to(DEV), other.int().to(DEV)
+    x, w = torch.randn(5, C, generator=g).to(BF).to(DEV), torch.rand(C, generator=g).to(DEV)
+    W, bits = torch.randn(64, C, generator=g).to(BF).to(DEV), torch.full((64, C // 32), 0x66666666, dtype=torch.int32, device=DEV)
+    for dtype in (BF, F8):
+        a, b = (lcp.RMSNorm(w, perm=p, dtype=dtype)(x) for p in (perm, other))
+        assert torch.equal(a[0].view(torch.uint8), b[0].view(torch.uint8)) and (a[1] is None or torch.equal(a[1], b[1]))
+        a, b = (lcp.SparseLinear.pack(W, p, bits, dtype=dtype) for p in (perm, other))
+        assert torch.equal(a.vals, b.vals) and torch.equal(a.meta, b.meta)
